@@ -21,6 +21,7 @@ Q5_K = 13
 Q6_K = 14
 Q3_K = 11
 IQ4_XS = 23
+F32, F16, BF16 = 0, 1, 30   # element types of the row operators
 BLOCK_VALUES = {Q4_0: 32, Q8_0: 32, Q4_K: 256, Q5_K: 256, Q6_K: 256, Q3_K: 256, IQ4_XS: 256}
 BLOCK_BYTES = {Q4_0: 18, Q8_0: 34, Q4_K: 144, Q5_K: 176, Q6_K: 210, Q3_K: 110, IQ4_XS: 136}
 Q8_1_BYTES = 36
@@ -86,6 +87,19 @@ _sig("qmm_plan_dense", _i32, _i32, _i64, _i64, _i64, ctypes.c_int32, ctypes.POIN
 _sig("qmm_tile_efficiency", ctypes.c_int32, _i64, ctypes.c_int32)
 _sig("qmm_select_tile_j", ctypes.c_int32, _i64)
 _sig("qmm_streamk_unit_start", _i64, _i64, _i64, _i64, _i64)
+_sig("qmm_sort_ids_workspace", _sz, _i64, _i64)
+_sig("qmm_sort_ids", _i32, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp)
+_sig("qmm_gather_sorted", _i32, _i32, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp)
+_sig("qmm_combine", _i32, _i32, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp)
+_sig("qmm_combine_backward", _i32, _i32, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp)
+_sig("qmm_embed", _i32, _i32, _vp, _i64, _i64, _vp, _i64, ctypes.c_float, _i32, _vp, _vp)
+_sig("qmm_embed_backward_workspace", _sz, _i64, _i64, _i64)
+_sig("qmm_embed_backward", _i32, _i32, _vp, _i64, _i64, _vp, _i64, ctypes.c_float, _i32, _vp, _vp, _sz, _vp)
+_sig("qmm_lora_workspace", _sz, _i64, _i64, _i64, _i64, _i64)
+_sig("qmm_lora", _i32, _i32, _i32, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp)
+_sig("qmm_lora_backward_workspace", _sz, _i64, _i64, _i64, _i64, _i64)
+_sig("qmm_lora_backward", _i32, _i32, _i32, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp,
+     _vp, _vp, _vp, _sz, _vp)
 _sig("qmm_matvec_kernel", _i32, _i32, _vp, _i64, _i64, _vp, _i64, _i32, ctypes.POINTER(_i32))
 
 
@@ -525,3 +539,271 @@ def debug_subdots(w, qtype, rows, k, xq, n, path):
     _check(_L.qmm_debug_subdots(qtype, pw, rows, k, px, n, path, ctypes.c_void_p(out.data_ptr()),
                                 ctypes.c_void_p(ws.data_ptr()), ws.numel(), _stream()))
     return out
+
+
+# --------------------------------------------------------------------------------------------
+# Row operators: embedding, expert gather / combine, low-rank adapters (and their gradients)
+# --------------------------------------------------------------------------------------------
+_ELEM_TYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+_ELEM_DTYPES = {v: d for d, v in _ELEM_TYPES.items()}
+
+
+def _elem(t, name):
+    """Element type of a contiguous fp32, fp16 or bf16 tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    e = _ELEM_TYPES.get(t.dtype)
+    if e is None:
+        raise TypeError(f"{name} must have dtype float32, float16 or bfloat16, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return e
+
+
+def _arg(t, dtype, shape, name):
+    """Address of a contiguous tensor of this dtype and shape (None: a null pointer)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _same_device(*tensors):
+    """Last check before pointers cross the C ABI: every tensor lives on the first one's device."""
+    dev = tensors[0].device
+    if dev.type != "cuda":
+        raise ValueError("every tensor must be a device tensor")
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"every tensor must be on {dev}, got {t.device}")
+    return dev
+
+
+def _ws_args(ws, nbytes, device):
+    """(address, bytes, tensor to keep until the launch) of a workspace of at least nbytes."""
+    if ws is None:
+        if nbytes == 0:
+            return None, 0, None
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    else:
+        _need(ws, torch.uint8, "ws")
+        _same_device(ws)
+    return ws.data_ptr(), ws.numel(), ws
+
+
+def sort_ids_workspace(n, n_keys):
+    return int(_L.qmm_sort_ids_workspace(n, n_keys))
+
+
+def sort_ids(ids, n_keys, ws=None):
+    """Stable sort of int32 ids (any shape).  Returns int32 (order [n], pos of ids' shape,
+    bounds [n_keys + 1]): indices by id with ids outside [0, n_keys) last, each index's place in
+    order (-1 for an id outside), and the start of each id's segment."""
+    n = ids.numel() if isinstance(ids, torch.Tensor) else 0
+    pi = _need(ids, torch.int32, "ids")
+    if n_keys < 1:
+        raise ValueError(f"n_keys must be >= 1, got {n_keys}")
+    dev = _same_device(ids)
+    order = torch.empty(n, dtype=torch.int32, device=dev)
+    pos = torch.empty_like(ids)
+    bounds = torch.empty(n_keys + 1, dtype=torch.int32, device=dev)
+    pw, nw, ws = _ws_args(ws, _L.qmm_sort_ids_workspace(n, n_keys), dev)
+    _check(_L.qmm_sort_ids(pi, n, n_keys, order.data_ptr(), pos.data_ptr(), bounds.data_ptr(), pw, nw, _stream()))
+    return order, pos, bounds
+
+
+def _valid_count(bounds):
+    """Address of the number of valid ids: the last entry of sort_ids' bounds."""
+    _need(bounds, torch.int32, "bounds")
+    if bounds.dim() != 1 or bounds.numel() < 2:
+        raise ValueError("bounds must be 1-D [n_keys + 1]")
+    return bounds.data_ptr() + 4 * (bounds.numel() - 1)
+
+
+def _need_pos(pos, name="pos"):
+    if pos.dim() != 2 or pos.shape[1] < 1:
+        raise ValueError(f"{name} must be 2-D [n_tok, top_k]")
+    return pos.shape
+
+
+def gather_sorted(x, pos, bounds, out=None):
+    """Rows to expert order: out[pos[t, j]] = x[t] for x [n_tok, k] and sort_ids' pos [n_tok, top_k];
+    rows of out [n_tok * top_k, k] past the valid pairs are zeros.  Its gradient: combine(d_out, pos)."""
+    e = _elem(x, "x")
+    pp = _need(pos, torch.int32, "pos")
+    n_tok, top_k = _need_pos(pos)
+    if x.dim() != 2 or x.shape[0] != n_tok:
+        raise ValueError(f"x must be [{n_tok}, k]")
+    k = x.shape[1]
+    nv = _valid_count(bounds)
+    if out is None:
+        out = torch.empty((n_tok * top_k, k), dtype=x.dtype, device=x.device)
+    po = _arg(out, x.dtype, (n_tok * top_k, k), "out")
+    _same_device(x, pos, bounds, out)
+    _check(_L.qmm_gather_sorted(e, x.data_ptr(), n_tok, top_k, k, pp, nv, po, _stream()))
+    return out
+
+
+def combine(h, pos=None, weights=None, base=None, out=None):
+    """out[t] = base[t] + sum over j of weights[t, j] * h[pos[t, j]].  h: [n_tok * top_k, k] in expert
+    order with pos int32 [n_tok, top_k] (entries outside the rows add nothing), or, without pos, in
+    (token, slot) order [n_tok, top_k, k] as matmul_id returns it.  weights: fp32 [n_tok, top_k]
+    (None: ones); base: [n_tok, k] or None; out may be base."""
+    e = _elem(h, "h")
+    if pos is None:
+        if h.dim() != 3 or h.shape[1] < 1:
+            raise ValueError("h must be 3-D [n_tok, top_k, k] where pos is None")
+        n_tok, top_k, k = h.shape
+        pp = None
+    else:
+        pp = _need(pos, torch.int32, "pos")
+        n_tok, top_k = _need_pos(pos)
+        if h.dim() != 2 or h.shape[0] != n_tok * top_k:
+            raise ValueError(f"h must be [{n_tok * top_k}, k]")
+        k = h.shape[1]
+    pw = _arg(weights, torch.float32, (n_tok, top_k), "weights")
+    pb = _arg(base, h.dtype, (n_tok, k), "base")
+    if out is None:
+        out = torch.empty((n_tok, k), dtype=h.dtype, device=h.device)
+    po = _arg(out, h.dtype, (n_tok, k), "out")
+    _same_device(h, pos, weights, base, out)
+    _check(_L.qmm_combine(e, h.data_ptr(), n_tok, top_k, k, pp, pw, pb, po, _stream()))
+    return out
+
+
+def combine_backward(dy, h, pos=None, weights=None, bounds=None):
+    """Gradient of combine: (dh of h's shape and dtype, fp32 dw [n_tok, top_k]); dy [n_tok, k].  With pos,
+    bounds is sort_ids' (rows of dh past the valid pairs are zeros).  The gradient of base is dy."""
+    e = _elem(h, "h")
+    if pos is None:
+        if h.dim() != 3 or h.shape[1] < 1:
+            raise ValueError("h must be 3-D [n_tok, top_k, k] where pos is None")
+        n_tok, top_k, k = h.shape
+        pp = nv = None
+    else:
+        pp = _need(pos, torch.int32, "pos")
+        n_tok, top_k = _need_pos(pos)
+        if h.dim() != 2 or h.shape[0] != n_tok * top_k:
+            raise ValueError(f"h must be [{n_tok * top_k}, k]")
+        k = h.shape[1]
+        nv = _valid_count(bounds)
+    pd = _arg(dy, h.dtype, (n_tok, k), "dy")
+    pw = _arg(weights, torch.float32, (n_tok, top_k), "weights")
+    dev = _same_device(h, dy, pos, weights, bounds)
+    dh = torch.empty_like(h)
+    dw = torch.empty((n_tok, top_k), dtype=torch.float32, device=dev)
+    _check(_L.qmm_combine_backward(e, pd, h.data_ptr(), n_tok, top_k, k, pp, pw, nv, dh.data_ptr(), dw.data_ptr(),
+                                   _stream()))
+    return dh, dw
+
+
+def embed(table, qtype, vocab, k, ids, scale=1.0, dtype=torch.float32, out=None):
+    """out[i] = scale * table[ids[i]] (zeros for an id outside [0, vocab)).  table: fp32, fp16 or bf16
+    [vocab, k] (qtype F32, F16, BF16), or uint8 rows of GGUF blocks; ids int32 of any shape; out
+    ids.shape + [k] of dtype.  With ids 0 .. vocab - 1 it expands a block-quantized matrix."""
+    pt = _need(table, _ELEM_DTYPES.get(qtype, torch.uint8), "table")
+    pi = _need(ids, torch.int32, "ids")
+    if qtype in _ELEM_DTYPES:
+        _need_size(table, vocab * k * table.element_size(), "table")
+    else:
+        _need_weights(table, qtype, vocab, k, "table")
+    if dtype not in _ELEM_TYPES:
+        raise TypeError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
+    shape = (*ids.shape, k)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=ids.device)
+    po = _arg(out, dtype, shape, "out")
+    _same_device(table, ids, out)
+    _check(_L.qmm_embed(qtype, pt, vocab, k, pi, ids.numel(), scale, _ELEM_TYPES[dtype], po, _stream()))
+    return out
+
+
+def embed_backward_workspace(n, k, vocab):
+    return int(_L.qmm_embed_backward_workspace(n, k, vocab))
+
+
+def embed_backward(dy, ids, vocab, scale=1.0, dtype=torch.float32, out=None, ws=None):
+    """Gradient of embed with respect to a table of elements: [vocab, k] of dtype, every row written;
+    dy: ids.shape + [k]."""
+    e = _elem(dy, "dy")
+    pi = _need(ids, torch.int32, "ids")
+    if dy.dim() < 1 or dy.shape[:-1] != ids.shape:
+        raise ValueError(f"dy must be {list(ids.shape)} + [k]")
+    if dtype not in _ELEM_TYPES:
+        raise TypeError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
+    if vocab < 1:
+        raise ValueError(f"vocab must be >= 1, got {vocab}")
+    n, k = ids.numel(), dy.shape[-1]
+    dev = _same_device(dy, ids, out)
+    if out is None:
+        out = torch.empty((vocab, k), dtype=dtype, device=dev)
+    po = _arg(out, dtype, (vocab, k), "out")
+    pw, nw, ws = _ws_args(ws, _L.qmm_embed_backward_workspace(n, k, vocab), dev)
+    _check(_L.qmm_embed_backward(e, dy.data_ptr(), n, k, pi, vocab, scale, _ELEM_TYPES[dtype], po, pw, nw, _stream()))
+    return out
+
+
+def _lora_shapes(x, a, b, ids, scale):
+    e, w = _elem(x, "x"), _elem(a, "a")
+    if x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("x must be [n, k], a [n_adapters, rank, k] and b [n_adapters, rows, rank]")
+    n, k = x.shape
+    na, rank, rows = a.shape[0], a.shape[1], b.shape[1]
+    _arg(a, a.dtype, (na, rank, k), "a")
+    _arg(b, a.dtype, (na, rows, rank), "b")
+    _arg(ids, torch.int32, (n,), "ids")
+    ps = _arg(scale, torch.float32, (na,), "scale")
+    return e, w, n, k, na, rank, rows, ps
+
+
+def lora_workspace(n, k, rows, rank, n_adapters):
+    return int(_L.qmm_lora_workspace(n, k, rows, rank, n_adapters))
+
+
+def lora(x, a, b, ids, scale=None, base=None, out=None, keep_h=False, ws=None):
+    """out[i] = base[i] + scale[c] * b[c] @ (a[c] @ x[i]) with c = ids[i]; base[i] alone for a c outside
+    [0, n_adapters).  x [n, k] and base, out [n, rows] of one dtype; a [n_adapters, rank, k] and
+    b [n_adapters, rows, rank] of x's dtype (beside fp32 x: any); ids int32 [n]; scale fp32
+    [n_adapters]; out may be base.  keep_h: returns (out, fp32 a[c] @ x[i] [n, rank]) for the backward."""
+    e, w, n, k, na, rank, rows, ps = _lora_shapes(x, a, b, ids, scale)
+    pb = _arg(base, x.dtype, (n, rows), "base")
+    dev = _same_device(x, a, b, ids, scale, base, out)
+    if out is None:
+        out = torch.empty((n, rows), dtype=x.dtype, device=dev)
+    po = _arg(out, x.dtype, (n, rows), "out")
+    h = torch.empty((n, rank), dtype=torch.float32, device=dev) if keep_h else None
+    pw, nw, ws = _ws_args(ws, _L.qmm_lora_workspace(n, k, rows, rank, na), dev)
+    _check(_L.qmm_lora(e, w, x.data_ptr(), n, k, a.data_ptr(), b.data_ptr(), rows, rank, na, ids.data_ptr(), ps, pb,
+                       po, h.data_ptr() if keep_h else None, pw, nw, _stream()))
+    return (out, h) if keep_h else out
+
+
+def lora_backward_workspace(n, k, rows, rank, n_adapters):
+    return int(_L.qmm_lora_backward_workspace(n, k, rows, rank, n_adapters))
+
+
+def lora_backward(x, dy, h, a, b, ids, scale=None, dx_base=None, need_dx=True, need_dw=True, ws=None):
+    """Gradient of lora: (dx [n, k] of x's dtype, fp32 da and db of a's and b's shapes).  h is what lora
+    kept; dx_base [n, k] or None is what the projection itself contributes to dx.  need_dx, need_dw:
+    False leaves dx, or da and db, out (None)."""
+    e, w, n, k, na, rank, rows, ps = _lora_shapes(x, a, b, ids, scale)
+    pd = _arg(dy, x.dtype, (n, rows), "dy")
+    ph = _arg(h, torch.float32, (n, rank), "h")
+    px = _arg(dx_base, x.dtype, (n, k), "dx_base")
+    dev = _same_device(x, a, b, ids, scale, dy, h, dx_base)
+    dx = torch.empty_like(x) if need_dx else None
+    da = torch.empty((na, rank, k), dtype=torch.float32, device=dev) if need_dw else None
+    db = torch.empty((na, rows, rank), dtype=torch.float32, device=dev) if need_dw else None
+    pw, nw, ws = _ws_args(ws, _L.qmm_lora_backward_workspace(n, k, rows, rank, na), dev)
+    _check(_L.qmm_lora_backward(e, w, x.data_ptr(), pd, ph, n, k, a.data_ptr(), b.data_ptr(), rows, rank, na,
+                                ids.data_ptr(), ps, px, dx.data_ptr() if need_dx else None,
+                                da.data_ptr() if need_dw else None, db.data_ptr() if need_dw else None, pw, nw,
+                                _stream()))
+    return dx, da, db

@@ -152,6 +152,43 @@ hipError_t launch_f16act_encode(const float *x, int64_t n, int64_t k, uint16_t *
 hipError_t launch_mmvq_f16act(int type, const uint8_t *w, int64_t rows, int64_t k, const uint16_t *y16,
                               const int32_t *e, const float *bsum, int64_t n, float *out, hipStream_t s);
 
+// Row operators (sort_ids.hip, combine.hip, embed.hip, lora.hip).  Types are the GGUF ids of include/qmm.h;
+// arguments are checked in api_rows.cpp.
+// Stable sort of n ids: order / pos (may be null) / bounds (may be null) as qmm_sort_ids.  with_keys: the
+// sorted keys (ids outside [0, n_keys) as n_keys) stay in ws, at sort_ids_keys.
+size_t sort_ids_bytes(int64_t n, int64_t n_keys, bool with_keys);
+const int32_t *sort_ids_keys(const void *ws, int64_t n, int64_t n_keys);
+hipError_t launch_sort_ids(const int32_t *ids, int64_t n, int64_t n_keys, int32_t *order, int32_t *pos,
+                           int32_t *bounds, bool with_keys, uint8_t *ws, hipStream_t s);
+hipError_t launch_gather_sorted(int type, const void *x, int64_t n_tok, int64_t top_k, int64_t k, const int32_t *pos,
+                                const int32_t *n_valid, void *y, hipStream_t s);
+hipError_t launch_combine(int type, const void *h, int64_t n_tok, int64_t top_k, int64_t k, const int32_t *pos,
+                          const float *w, const void *base, void *y, hipStream_t s);
+hipError_t launch_combine_backward(int type, const void *dy, const void *h, int64_t n_tok, int64_t top_k, int64_t k,
+                                   const int32_t *pos, const float *w, const int32_t *n_valid, void *dh, float *dw,
+                                   hipStream_t s);
+hipError_t launch_embed(int type, const void *table, int64_t vocab, int64_t k, const int32_t *ids, int64_t n,
+                        float scale, int y_type, void *y, hipStream_t s);
+size_t embed_backward_bytes(int64_t n, int64_t k, int64_t vocab);
+hipError_t launch_embed_backward(int dy_type, const void *dy, int64_t n, int64_t k, const int32_t *ids, int64_t vocab,
+                                 float scale, int g_type, void *grad, uint8_t *ws, hipStream_t s);
+// What the adapters' forward and backward calls have in common.
+struct LoraCall {
+    int x_type, w_type;
+    const void *x;      // [n][k]
+    int64_t n, k;
+    const void *a;      // [n_adapters][rank][k]
+    const void *b;      // [n_adapters][rows][rank]
+    int64_t rows, rank, n_adapters;
+    const int32_t *ids; // [n]
+    const float *scale; // [n_adapters] or null (1)
+};
+size_t lora_bytes(int64_t n, int64_t k, int64_t rows, int64_t rank, int64_t n_adapters);
+hipError_t launch_lora(const LoraCall &c, const void *base, void *y, float *h_out, uint8_t *ws, hipStream_t s);
+size_t lora_backward_bytes(int64_t n, int64_t k, int64_t rows, int64_t rank, int64_t n_adapters);
+hipError_t launch_lora_backward(const LoraCall &c, const void *dy, const float *h, const void *dx_base, void *dx,
+                                float *da, float *db, uint8_t *ws, hipStream_t s);
+
 // Dense fp32-input product with a workspace sized exactly to its plan (api.cpp), for the
 // allocation-free entry point (noalloc.hip).  o: one reading of the overrides for the whole call.
 Ovr load_overrides();

@@ -60,7 +60,8 @@ typedef enum {
 } qmm_status;
 
 typedef enum {
-    QMM_Q4_0 = 2, QMM_Q8_0 = 8, QMM_Q3_K = 11, QMM_Q4_K = 12, QMM_Q5_K = 13, QMM_Q6_K = 14, QMM_IQ4_XS = 23
+    QMM_Q4_0 = 2, QMM_Q8_0 = 8, QMM_Q3_K = 11, QMM_Q4_K = 12, QMM_Q5_K = 13, QMM_Q6_K = 14, QMM_IQ4_XS = 23,
+    QMM_F32 = 0, QMM_F16 = 1, QMM_BF16 = 30   /* row operators only (qmm_embed and the calls after it) */
 } qmm_type; /* GGUF type ids */
 
 /* Message for the last non-OK status returned on this thread ("" if none). */
@@ -237,6 +238,88 @@ size_t qmm_matmul_id_glu_workspace(int type, int64_t n_exp, int64_t rows, int64_
 qmm_status qmm_matmul_id_glu(int type, const void *w_gate, const void *w_up, int64_t n_exp, int64_t rows,
                              int64_t k, const float *x, const int32_t *ids, int64_t n_tok, int64_t top_k,
                              float *y, void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Row operators: what a model does with rows that an id picks, around the products above --
+ * embedding lookup, the way to the experts and back, low-rank adapters -- with their gradients.
+ *  - Element types are QMM_F32, QMM_F16 or QMM_BF16; sums are taken in fp32 and rounded once, to
+ *    nearest even, at the store.  Every result is bitwise reproducible (no atomic decides an order).
+ *  - ids are int32.  An id outside its range (such as -1) picks no row: padding tokens, dropped
+ *    (token, slot) pairs, rows without an adapter.  Row contents that no id picks are not read into
+ *    any sum, so NaN there stays there.
+ *  - Pointers need the alignment of their element (QMM_ERR_ARG otherwise; blocks 2 bytes); rows of
+ *    a multiple of 16 bytes at 16-byte aligned pointers are read and written faster.
+ *  - Row lengths (k, rows) are 1 .. 1<<20, counts (n, n_tok * top_k) 0 .. 1<<30; longer: QMM_ERR_SHAPE.
+ *    A count of 0 is a no-op, except that gradients and bounds are written as zeros.
+ *  - Workspaces (ws, 256-byte aligned) need no clearing and hold nothing between calls.
+ *
+ * qmm_sort_ids: the stable sort of n ids (expert or adapter of each (token, slot) pair, token of
+ *   each row).  order [n]: indices by id, equal ids in their own order, ids outside [0, n_keys)
+ *   last; pos [n]: the place of each index in order, -1 for an id outside; bounds [n_keys + 1]: the
+ *   segment of id v is order[bounds[v] .. bounds[v + 1]), bounds[n_keys] = number of valid ids.
+ *   1 <= n_keys <= 1<<30.  pos may be NULL.
+ * qmm_gather_sorted: rows to expert order: y[pos[t * top_k + j]] = x[t] for the token's top_k
+ *   slots; rows of y from *n_valid on become zeros.  x [n_tok][k], y [n_tok * top_k][k], pos as
+ *   qmm_sort_ids wrote it for the ids [n_tok][top_k], n_valid its bounds + n_keys (device).  Its
+ *   gradient is qmm_combine without weights.
+ * qmm_combine: and back: y[t] = base[t] + sum over j of w[t][j] * h[pos[t][j]].  h [n_tok * top_k][k];
+ *   pos int32 [n_tok][top_k], entries outside [0, n_tok * top_k) add nothing; pos NULL: h is in
+ *   (token, slot) order, as qmm_matmul_id writes it.  w fp32 [n_tok][top_k], or NULL for ones;
+ *   base [n_tok][k] (a shared expert's result, the residual) or NULL; y may be base.
+ * qmm_combine_backward: dh[pos[t][j]] = w[t][j] * dy[t], dw[t][j] = <dy[t], h[pos[t][j]]> (fp32;
+ *   0 where pos names no row); rows of dh from *n_valid on become zeros.  pos entries must differ
+ *   from each other; n_valid is not read where pos is NULL.  (The gradient of base is dy.)
+ * ------------------------------------------------------------------------------------------- */
+size_t qmm_sort_ids_workspace(int64_t n, int64_t n_keys);
+qmm_status qmm_sort_ids(const int32_t *ids, int64_t n, int64_t n_keys, int32_t *order, int32_t *pos,
+                        int32_t *bounds, void *ws, size_t ws_bytes, void *stream);
+qmm_status qmm_gather_sorted(int type, const void *x, int64_t n_tok, int64_t top_k, int64_t k, const int32_t *pos,
+                             const int32_t *n_valid, void *y, void *stream);
+qmm_status qmm_combine(int type, const void *h, int64_t n_tok, int64_t top_k, int64_t k, const int32_t *pos,
+                       const float *w, const void *base, void *y, void *stream);
+qmm_status qmm_combine_backward(int type, const void *dy, const void *h, int64_t n_tok, int64_t top_k, int64_t k,
+                                const int32_t *pos, const float *w, const int32_t *n_valid, void *dh, float *dw,
+                                void *stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * qmm_embed: y[i] = scale * table[ids[i]], zeros for an id outside [0, vocab).  table [vocab][k] of
+ *   any type: elements, or rows of GGUF blocks (k a multiple of the block size), decoded as the
+ *   products' weights are; y [n][k] of y_type.  With ids 0 .. vocab - 1 it expands a weight matrix.
+ * qmm_embed_backward: grad[v] = scale * sum of dy[i] over the rows i with ids[i] = v, all vocab rows
+ *   written (zeros where no id picks them).  dy [n][k] of dy_type, grad [vocab][k] of g_type.
+ *   vocab <= 1<<30.
+ * ------------------------------------------------------------------------------------------- */
+qmm_status qmm_embed(int type, const void *table, int64_t vocab, int64_t k, const int32_t *ids, int64_t n,
+                     float scale, int y_type, void *y, void *stream);
+size_t qmm_embed_backward_workspace(int64_t n, int64_t k, int64_t vocab);
+qmm_status qmm_embed_backward(int dy_type, const void *dy, int64_t n, int64_t k, const int32_t *ids, int64_t vocab,
+                              float scale, int g_type, void *grad, void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a shared projection (qmm_matmul's result as base):
+ * qmm_lora: y[i] = base[i] + scale[c] * B[c] (A[c] x[i]), c = ids[i]; y[i] = base[i] for a c outside
+ *   [0, n_adapters).  x [n][k] and base, y [n][rows] of x_type; a [n_adapters][rank][k] and
+ *   b [n_adapters][rows][rank] of w_type, which is x_type or, beside fp32 x, any element type;
+ *   1 <= rank <= 128 (adapters of a lower rank are filled up with zeros); scale fp32 [n_adapters] or
+ *   NULL for ones; base NULL: zeros; y may be base.  h fp32 [n][rank] or NULL: receives A[c] x[i]
+ *   (zeros without an adapter) for the backward call.
+ * qmm_lora_backward: with dh[i] = scale[c] * B[c]^T dy[i]:
+ *   dx[i] = dx_base[i] + A[c]^T dh[i] (x_type [n][k]; dx_base NULL: zeros; dx may be dx_base),
+ *   da[c] = sum of dh[i] x[i]^T (fp32 [n_adapters][rank][k]),
+ *   db[c] = scale[c] * sum of dy[i] h[i]^T (fp32 [n_adapters][rows][rank]),
+ *   over the rows i of adapter c; zeros for an adapter without rows.  dx, da and db may each be NULL
+ *   (not computed).
+ * n_adapters <= 1<<20, n_adapters * rank * max(k, rows) <= 1<<40.
+ * ------------------------------------------------------------------------------------------- */
+size_t qmm_lora_workspace(int64_t n, int64_t k, int64_t rows, int64_t rank, int64_t n_adapters);
+qmm_status qmm_lora(int x_type, int w_type, const void *x, int64_t n, int64_t k, const void *a, const void *b,
+                    int64_t rows, int64_t rank, int64_t n_adapters, const int32_t *ids, const float *scale,
+                    const void *base, void *y, float *h, void *ws, size_t ws_bytes, void *stream);
+size_t qmm_lora_backward_workspace(int64_t n, int64_t k, int64_t rows, int64_t rank, int64_t n_adapters);
+qmm_status qmm_lora_backward(int x_type, int w_type, const void *x, const void *dy, const float *h, int64_t n,
+                             int64_t k, const void *a, const void *b, int64_t rows, int64_t rank,
+                             int64_t n_adapters, const int32_t *ids, const float *scale, const void *dx_base,
+                             void *dx, float *da, float *db, void *ws, size_t ws_bytes, void *stream);
 
 /* ---------------------------------------------------------------------------------------------
  * Test hook: the integer sub-block dots from the production kernels ([MMQ] "write-back": the
