@@ -18,7 +18,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libqmm.so")
 PROBE_LIB = os.path.join(HERE, "libqmm_probe.so")   # measurement probes for bench.py (include/qmm_probe.h)
 SOURCES = ["quantize.hip", "mmvq.hip", "mmvq_stream.hip", "mmvq_dot4.hip", "mmq.hip", "moe.hip", "f16act.hip",
-           "noalloc.hip", "repack.hip", "sort_ids.hip", "combine.hip", "embed.hip", "lora.hip", "api.cpp", "api_rows.cpp"]
+           "noalloc.hip", "repack.hip", "sort_ids.hip", "combine.hip", "embed.hip", "lora.hip", "lora_narrow.hip", "lora_wide.hip",
+           "lora_outer.hip", "api.cpp", "api_rows.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

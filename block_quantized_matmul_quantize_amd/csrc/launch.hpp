@@ -183,6 +183,23 @@ struct LoraCall {
     const int32_t *ids; // [n]
     const float *scale; // [n_adapters] or null (1)
 };
+// Padded rank of the partial and dh rows; slices of K that a product of k values a row is split into.
+int lora_padded_rank(int64_t rank);
+int lora_narrow_slices(int64_t n, int64_t k);
+// part [slices][n][padded rank] = v [n][k] times the row's matrix: m [rank][k] (by_row) or [k][rank] of each adapter.
+hipError_t launch_lora_narrow(int x_type, int w_type, bool by_row, const void *v, int64_t n, int64_t k, const void *m,
+                              int64_t rank, int64_t n_adapters, const int32_t *ids, float *part, hipStream_t s);
+// out [n][cols] = base + scale * (sum of part's slices) times m [rank][cols] (by_row) or [cols][rank]; h (may be
+// null): the sum, scaled where scale_h; out null: h alone.
+hipError_t launch_lora_wide(int x_type, int w_type, bool by_row, const float *part, int parts, int64_t n, int64_t cols,
+                            const void *m, int64_t rank, int64_t n_adapters, const int32_t *ids, const float *scale,
+                            const void *base, void *out, float *h, int64_t h_stride, bool scale_h, hipStream_t s);
+size_t lora_outer_bytes(int64_t n, int64_t k, int64_t rows, int64_t rank, int64_t n_adapters);
+// da [n_adapters][rank][k] from x, dh and db [n_adapters][rows][rank] from dy, h (either may be null).
+hipError_t launch_lora_outer(int x_type, const void *x, const float *dh, int64_t dh_stride, int64_t k, float *da,
+                             const void *dy, const float *h, int64_t rows, const float *scale, float *db, int64_t n,
+                             int64_t rank, int64_t n_adapters, const int32_t *order, const int32_t *bounds, float *part,
+                             hipStream_t s);
 size_t lora_bytes(int64_t n, int64_t k, int64_t rows, int64_t rank, int64_t n_adapters);
 hipError_t launch_lora(const LoraCall &c, const void *base, void *y, float *h_out, uint8_t *ws, hipStream_t s);
 size_t lora_backward_bytes(int64_t n, int64_t k, int64_t rows, int64_t rank, int64_t n_adapters);

@@ -1,0 +1,218 @@
+// Gradients of the adapters' matrices: da[c][r][j] = sum of dh[i][r] * x[i][j] and db[c][o][r] =
+// scale[c] * sum of dy[i][o] * h[i][r] over the rows i of adapter c, both in one launch.
+//
+// A workgroup takes 64 or 128 columns of x (or dy) for all ranks of one adapter; its four waves take
+// turns at 32 of the adapter's rows (of a list sorted by adapter).  x and dy are read once; K of the
+// products is the row, so every lane reads 8 rows of 4 or 8 neighbouring columns and is itself the
+// transpose that the operand needs, without LDS.  h and dh, at most 128 values a row, come from L2,
+// once for each block of columns.  The waves add their sums up in LDS in a fixed order.  An adapter
+// with many rows and few columns is split over several workgroups, whose sums a second launch adds up.
+#include "launch.hpp"
+#include "lora_parts.hpp"
+
+namespace qmm {
+
+namespace {
+
+struct Job {
+    const void *v;
+    const float *h;
+    float *out;
+    const float *scale;     // or null
+    int64_t cols, h_stride, slices;
+    int32_t by_row, h_vec;  // out [rank][cols], else [cols][rank]
+};
+struct Args {
+    Job job[2];
+    const int32_t *order, *bounds;
+    float *part;            // [splits][n_adapters * rank * (all columns)], where splits > 1
+    int64_t items, out_total;
+    int32_t rank, splits, n_adapters;
+};
+
+template <class X, int RT> constexpr int kCols = sizeof(X) == 4 || RT == 8 ? 4 : 8;   // a lane's columns
+
+template <class X, int RT, bool VV>
+__global__ __launch_bounds__(256) void outer_kernel(Args a) {
+    constexpr int V = kCols<X, RT>, C = 16 * V, R = 16 * RT;
+    __shared__ float sum[R][C + 4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, m = lane & 15, g = lane >> 4;
+    for (int64_t item = blockIdx.x; item < a.items; item += gridDim.x) {
+        // (adapter, job, block of columns, split of the rows)
+        const int64_t per = (a.job[0].slices + a.job[1].slices) * a.splits;
+        const int64_t c = item / per;
+        int64_t u = item - c * per;
+        const int split = (int)(u % a.splits);
+        u /= a.splits;
+        const int which = u < a.job[0].slices ? 0 : 1;
+        const Job &job = a.job[which];
+        const int64_t col0 = (which ? u - a.job[0].slices : u) * C;
+        const int64_t lo = a.bounds[c], hi = a.bounds[c + 1];
+        const X *v = (const X *)job.v;
+        // columns and ranks past the last repeat valid ones: their sums are not used
+        const int64_t left = job.cols - col0 - V * m;
+        const int64_t col = left >= V || (!VV && left > 0) ? col0 + V * m : VV ? job.cols - V : job.cols - 1;
+        const int nc = left >= V ? V : left > 0 ? (int)left : VV ? V : 1;
+        const int r0 = RT * m + RT <= a.rank ? RT * m : job.h_vec ? a.rank - RT : RT * m < a.rank ? RT * m : a.rank - 1;
+        const int nr = a.rank - r0;
+        f32x4 acc[RT][V];
+#pragma unroll
+        for (int p = 0; p < RT; ++p)
+#pragma unroll
+            for (int q = 0; q < V; ++q) acc[p][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const int64_t step = (int64_t)a.splits * 4 * 32;
+        for (int64_t p0 = lo + (split * 4 + wave) * 32; p0 < hi; p0 += step) {
+            const int64_t at = p0 + (lane & 31);
+            const int32_t idx = a.order[at < hi ? at : hi - 1];
+            Rows8<X, V> xs;
+            Rows8<float, RT> hr;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int64_t i = __shfl(idx, 8 * g + e);
+                xs.row[e] = load_row<VV, V>(v + i * job.cols + col, nc);
+                if (job.h_vec) hr.row[e] = load_row<true, RT>(job.h + i * job.h_stride + r0, RT);
+                else hr.row[e] = load_row<false, RT>(job.h + i * job.h_stride + r0, nr);
+            }
+            if (p0 + 32 > hi) {   // rows past the adapter's last
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (p0 + 8 * g + e >= hi) {
+#pragma unroll
+                        for (int q = 0; q < V; ++q) xs.row[e].v[q] = (X)0.f;
+#pragma unroll
+                        for (int p = 0; p < RT; ++p) hr.row[e].v[p] = 0.f;
+                    }
+            }
+            Frag<3> hf[RT];
+#pragma unroll
+            for (int p = 0; p < RT; ++p) hf[p] = parts_of<false>(hr.column(p));
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                const auto xf = parts_of<false>(xs.column(q));
+#pragma unroll
+                for (int p = 0; p < RT; ++p) acc[p][q] = mul_acc<bf16_t>(hf[p], xf, acc[p][q]);
+            }
+        }
+        // acc[p][q] element e: rank RT * (4g + e) + p, column col0 + V * m + q
+        for (int w = 0; w < 4; ++w) {
+            if (wave == w) {
+#pragma unroll
+                for (int p = 0; p < RT; ++p)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float *s = &sum[RT * (4 * g + e) + p][V * m];
+#pragma unroll
+                        for (int q = 0; q < V; ++q) s[q] = w ? s[q] + acc[p][q][e] : acc[p][q][e];
+                    }
+            }
+            __syncthreads();
+        }
+        const float scale = job.scale ? job.scale[c] : 1.f;
+        const int64_t cols = job.cols - col0 < C ? job.cols - col0 : C;
+        const int64_t first = which ? (int64_t)a.n_adapters * a.rank * a.job[0].cols : 0;
+        float *out = a.splits > 1 ? a.part + split * a.out_total + first : job.out;
+        if (job.by_row) {
+            for (int j = threadIdx.x; j < a.rank * C; j += 256) {
+                const int r = j / C, k = j % C;
+                if (k < cols) out[(c * a.rank + r) * job.cols + col0 + k] = sum[r][k] * scale;
+            }
+        } else {
+            out += (c * job.cols + col0) * a.rank;
+            for (int k = threadIdx.x / R; k < cols; k += 256 / R) {
+                const int r = threadIdx.x % R;
+                if (r < a.rank) out[k * a.rank + r] = sum[r][k] * scale;
+            }
+        }
+        __syncthreads();
+    }
+}
+
+__global__ __launch_bounds__(256) void join_kernel(const float *__restrict__ part, int splits, int64_t n0, int64_t total,
+                                                   float *__restrict__ out0, float *__restrict__ out1) {
+    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < total; t += (int64_t)gridDim.x * 256) {
+        float s = 0.f;
+#pragma unroll 4
+        for (int p = 0; p < splits; ++p) s += part[p * total + t];
+        (t < n0 ? out0[t] : out1[t - n0]) = s;
+    }
+}
+
+
+
+// Workgroups an adapter's rows are split over: 512 in all, while each wave keeps two steps of the
+// average adapter's rows.
+int splits_of(int64_t n, int64_t n_adapters, int64_t blocks) {
+    int64_t s = 512 / (blocks * n_adapters), most = n / n_adapters / 256;
+    if (s > most) s = most;
+    return s < 1 ? 1 : s > 16 ? 16 : (int)s;
+}
+int rank_tiles(int64_t rank) { return lora_padded_rank(rank) / 16; }
+int64_t block_cols(int x_type, int rt) { return x_type == kF32 || rt == 8 ? 64 : 128; }
+int64_t blocks_of(int x_type, int64_t rank, int64_t cols) {
+    const int64_t c = block_cols(x_type, rank_tiles(rank));
+    return (cols + c - 1) / c;
+}
+
+}  // namespace
+
+size_t lora_outer_bytes(int64_t n, int64_t k, int64_t rows, int64_t rank, int64_t n_adapters) {
+    // for any element type, and either gradient alone: no workgroup count is below the widest blocks'
+    size_t most = 0;
+    for (int which = 1; which < 4; ++which) {
+        const int64_t c = (which & 1 ? k : 0) + (which & 2 ? rows : 0);
+        const int64_t blocks = (which & 1 ? blocks_of(kBF16, rank, k) : 0) + (which & 2 ? blocks_of(kBF16, rank, rows) : 0);
+        const int s = splits_of(n, n_adapters, blocks);
+        const size_t bytes = s > 1 ? (size_t)s * n_adapters * rank * c * 4 : 0;
+        if (bytes > most) most = bytes;
+    }
+    return most;
+}
+
+hipError_t launch_lora_outer(int x_type, const void *x, const float *dh, int64_t dh_stride, int64_t k, float *da,
+                             const void *dy, const float *h, int64_t rows, const float *scale, float *db, int64_t n,
+                             int64_t rank, int64_t n_adapters, const int32_t *order, const int32_t *bounds, float *part,
+                             hipStream_t s) {
+    Args a{};
+    a.job[0] = Job{x, dh, da, nullptr, da ? k : 0, dh_stride, 0, 1, 0};
+    a.job[1] = Job{dy, h, db, scale, db ? rows : 0, rank, 0, 0, 0};
+    a.order = order;
+    a.bounds = bounds;
+    a.part = part;
+    a.rank = (int32_t)rank;
+    a.n_adapters = (int32_t)n_adapters;
+    const int rt = rank_tiles(rank);
+    int64_t blocks = 0;
+    for (Job &j : a.job) {
+        j.slices = blocks_of(x_type, rank, j.cols);
+        j.h_vec = rank % rt == 0 && j.h_stride % rt == 0 && (uintptr_t)j.h % (rt * 4 < 16 ? rt * 4 : 16) == 0;
+        blocks += j.slices;
+    }
+    a.splits = splits_of(n, n_adapters, blocks);
+    a.items = n_adapters * blocks * a.splits;
+    a.out_total = n_adapters * rank * (a.job[0].cols + a.job[1].cols);
+    hipError_t e = with_type(x_type, [&](auto t) -> hipError_t {
+        typedef decltype(t) X;
+        const dim3 grid((unsigned)(a.items < 1 << 22 ? a.items : 1 << 22));
+        auto go = [&](auto r) -> hipError_t {
+            constexpr int RT = decltype(r)::value;
+            constexpr int V = kCols<X, RT>;
+            const bool vv = a.job[0].cols % V == 0 && a.job[1].cols % V == 0 && aligned16(da ? x : nullptr, db ? dy : nullptr);
+            if (vv) hipLaunchKernelGGL((outer_kernel<X, RT, true>), grid, dim3(256), 0, s, a);
+            else hipLaunchKernelGGL((outer_kernel<X, RT, false>), grid, dim3(256), 0, s, a);
+            return hipGetLastError();
+        };
+        switch (rt) {
+            case 1: return go(std::integral_constant<int, 1>{});
+            case 2: return go(std::integral_constant<int, 2>{});
+            case 4: return go(std::integral_constant<int, 4>{});
+            default: return go(std::integral_constant<int, 8>{});
+        }
+    });
+    if (e != hipSuccess || a.splits == 1) return e;
+    const int64_t n0 = n_adapters * rank * a.job[0].cols, b = (a.out_total + 255) / 256;
+    hipLaunchKernelGGL(join_kernel, dim3((unsigned)(b < 65536 ? b : 65536)), dim3(256), 0, s, part, a.splits, n0,
+                       a.out_total, da, db);
+    return hipGetLastError();
+}
+
+}  // namespace qmm
