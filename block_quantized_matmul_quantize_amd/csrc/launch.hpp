@@ -189,15 +189,32 @@ int lora_narrow_slices(int64_t n, int64_t k);
 // part [slices][n][padded rank] = v [n][k] times the row's matrix: m [rank][k] (by_row) or [k][rank] of each adapter.
 hipError_t launch_lora_narrow(int x_type, int w_type, bool by_row, const void *v, int64_t n, int64_t k, const void *m,
                               int64_t rank, int64_t n_adapters, const int32_t *ids, float *part, hipStream_t s);
-// out [n][cols] = base + scale * (sum of part's slices) times m [rank][cols] (by_row) or [cols][rank]; h (may be
-// null): the sum, scaled where scale_h; out null: h alone.
+// Between the two halves: sums of the slices, and what the gradients of A and B need.
+struct LoraFinish {
+    const float *part;      // or null: only kept
+    int parts;
+    int64_t n, rank, n_adapters;
+    const int32_t *ids;
+    const float *scale;
+    float *sum;             // or null: [n][padded rank] (may be part: its first slice)
+    float *h;               // or null: [n][rank], zeros for a row without an adapter
+    // where not null, the bf16 parts [3][padded rank][lora_parts_stride(n)] of kept [n][rank] and of the scaled sum,
+    // rows at their places pos of the order sorted by adapter
+    const float *kept;
+    uint16_t *parts_h, *parts_dh;
+    const int32_t *pos;
+};
+hipError_t launch_lora_finish(const LoraFinish &c, hipStream_t s);
+// out [n][cols] = base + scale * (sum of part's slices) times m, [rank][cols] (by_row) or [cols][rank].
 hipError_t launch_lora_wide(int x_type, int w_type, bool by_row, const float *part, int parts, int64_t n, int64_t cols,
                             const void *m, int64_t rank, int64_t n_adapters, const int32_t *ids, const float *scale,
-                            const void *base, void *out, float *h, int64_t h_stride, bool scale_h, hipStream_t s);
+                            const void *base, void *out, hipStream_t s);
+// Row stride of the parts.
+int64_t lora_parts_stride(int64_t n);
 size_t lora_outer_bytes(int64_t n, int64_t k, int64_t rows, int64_t rank, int64_t n_adapters);
-// da [n_adapters][rank][k] from x, dh and db [n_adapters][rows][rank] from dy, h (either may be null).
-hipError_t launch_lora_outer(int x_type, const void *x, const float *dh, int64_t dh_stride, int64_t k, float *da,
-                             const void *dy, const float *h, int64_t rows, const float *scale, float *db, int64_t n,
+// da [n_adapters][rank][k] from x and dh's parts, db [n_adapters][rows][rank] from dy and h's (either may be null).
+hipError_t launch_lora_outer(int x_type, const void *x, const uint16_t *parts_dh, int64_t k, float *da, const void *dy,
+                             const uint16_t *parts_h, int64_t rows, const float *scale, float *db, int64_t n,
                              int64_t rank, int64_t n_adapters, const int32_t *order, const int32_t *bounds, float *part,
                              hipStream_t s);
 size_t lora_bytes(int64_t n, int64_t k, int64_t rows, int64_t rank, int64_t n_adapters);

@@ -2,10 +2,10 @@
 // scale[c] * sum of dy[i][o] * h[i][r] over the rows i of adapter c, both in one launch.
 //
 // A workgroup takes 64 or 128 columns of x (or dy) for all ranks of one adapter; its four waves take
-// turns at 32 of the adapter's rows (of a list sorted by adapter).  x and dy are read once; K of the
-// products is the row, so every lane reads 8 rows of 4 or 8 neighbouring columns and is itself the
-// transpose that the operand needs, without LDS.  h and dh, at most 128 values a row, come from L2,
-// once for each block of columns.  The waves add their sums up in LDS in a fixed order.  An adapter
+// turns at 32 places of the rows sorted by adapter.  x and dy are read once; K of the products is the
+// row, so every lane reads 8 rows of 4 or 8 neighbouring columns and is itself the transpose that the
+// operand needs, without LDS.  h and dh come as bf16 parts [3][rank][place], operands as they are, from
+// L2, once for each block of columns.  The waves add their sums up in LDS in a fixed order.  An adapter
 // with many rows and few columns is split over several workgroups, whose sums a second launch adds up.
 #include "launch.hpp"
 #include "lora_parts.hpp"
@@ -16,17 +16,17 @@ namespace {
 
 struct Job {
     const void *v;
-    const float *h;
+    const uint16_t *h;      // bf16 parts [3][padded rank][stride]
     float *out;
     const float *scale;     // or null
-    int64_t cols, h_stride, slices;
-    int32_t by_row, h_vec;  // out [rank][cols], else [cols][rank]
+    int64_t cols, slices;
+    int32_t by_row;         // out [rank][cols], else [cols][rank]
 };
 struct Args {
     Job job[2];
     const int32_t *order, *bounds;
     float *part;            // [splits][n_adapters * rank * (all columns)], where splits > 1
-    int64_t items, out_total;
+    int64_t items, out_total, stride;
     int32_t rank, splits, n_adapters;
 };
 
@@ -53,39 +53,45 @@ __global__ __launch_bounds__(256) void outer_kernel(Args a) {
         const int64_t left = job.cols - col0 - V * m;
         const int64_t col = left >= V || (!VV && left > 0) ? col0 + V * m : VV ? job.cols - V : job.cols - 1;
         const int nc = left >= V ? V : left > 0 ? (int)left : VV ? V : 1;
-        const int r0 = RT * m + RT <= a.rank ? RT * m : job.h_vec ? a.rank - RT : RT * m < a.rank ? RT * m : a.rank - 1;
-        const int nr = a.rank - r0;
         f32x4 acc[RT][V];
 #pragma unroll
         for (int p = 0; p < RT; ++p)
 #pragma unroll
             for (int q = 0; q < V; ++q) acc[p][q] = f32x4{0.f, 0.f, 0.f, 0.f};
         const int64_t step = (int64_t)a.splits * 4 * 32;
-        for (int64_t p0 = lo + (split * 4 + wave) * 32; p0 < hi; p0 += step) {
+        // steps at multiples of 32 places; an adapter without rows has none (its lo may be past the last row)
+        for (int64_t p0 = lo < hi ? lo / 32 * 32 + (split * 4 + wave) * 32 : hi; p0 < hi; p0 += step) {
             const int64_t at = p0 + (lane & 31);
-            const int32_t idx = a.order[at < hi ? at : hi - 1];
+            const int32_t idx = a.order[at < lo ? lo : at < hi ? at : hi - 1];
             Rows8<X, V> xs;
-            Rows8<float, RT> hr;
+            Frag<3> hf[RT];
+#pragma unroll
+            for (int p = 0; p < RT; ++p)
+#pragma unroll
+                for (int j = 0; j < 3; ++j)
+                    hf[p].p[j] = *(const u32x4 *)(job.h + (j * R + 16 * p + m) * a.stride + p0 + 8 * g);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int64_t i = __shfl(idx, 8 * g + e);
                 xs.row[e] = load_row<VV, V>(v + i * job.cols + col, nc);
-                if (job.h_vec) hr.row[e] = load_row<true, RT>(job.h + i * job.h_stride + r0, RT);
-                else hr.row[e] = load_row<false, RT>(job.h + i * job.h_stride + r0, nr);
             }
-            if (p0 + 32 > hi) {   // rows past the adapter's last
+            if (p0 < lo || p0 + 32 > hi) {   // places of other adapters
+                u32x4 keep;
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (p0 + 8 * g + e >= hi) {
+                for (int e = 0; e < 8; ++e) {
+                    const int64_t place = p0 + 8 * g + e;
+                    const bool mine = place >= lo && place < hi;
+                    const uint32_t half = mine ? 0xffffu : 0;
+                    keep[e / 2] = e & 1 ? keep[e / 2] | half << 16 : half;
+                    if (!mine)
 #pragma unroll
                         for (int q = 0; q < V; ++q) xs.row[e].v[q] = (X)0.f;
+                }
 #pragma unroll
-                        for (int p = 0; p < RT; ++p) hr.row[e].v[p] = 0.f;
-                    }
+                for (int p = 0; p < RT; ++p)
+#pragma unroll
+                    for (int j = 0; j < 3; ++j) hf[p].p[j] &= keep;
             }
-            Frag<3> hf[RT];
-#pragma unroll
-            for (int p = 0; p < RT; ++p) hf[p] = parts_of<false>(hr.column(p));
 #pragma unroll
             for (int q = 0; q < V; ++q) {
                 const auto xf = parts_of<false>(xs.column(q));
@@ -93,14 +99,14 @@ __global__ __launch_bounds__(256) void outer_kernel(Args a) {
                 for (int p = 0; p < RT; ++p) acc[p][q] = mul_acc<bf16_t>(hf[p], xf, acc[p][q]);
             }
         }
-        // acc[p][q] element e: rank RT * (4g + e) + p, column col0 + V * m + q
+        // acc[p][q] element e: rank 16 * p + 4g + e, column col0 + V * m + q
         for (int w = 0; w < 4; ++w) {
             if (wave == w) {
 #pragma unroll
                 for (int p = 0; p < RT; ++p)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float *s = &sum[RT * (4 * g + e) + p][V * m];
+                        float *s = &sum[16 * p + 4 * g + e][V * m];
 #pragma unroll
                         for (int q = 0; q < V; ++q) s[q] = w ? s[q] + acc[p][q][e] : acc[p][q][e];
                     }
@@ -155,6 +161,8 @@ int64_t blocks_of(int x_type, int64_t rank, int64_t cols) {
 
 }  // namespace
 
+int64_t lora_parts_stride(int64_t n) { return (n + 31) / 32 * 32; }
+
 size_t lora_outer_bytes(int64_t n, int64_t k, int64_t rows, int64_t rank, int64_t n_adapters) {
     // for any element type, and either gradient alone: no workgroup count is below the widest blocks'
     size_t most = 0;
@@ -168,23 +176,23 @@ size_t lora_outer_bytes(int64_t n, int64_t k, int64_t rows, int64_t rank, int64_
     return most;
 }
 
-hipError_t launch_lora_outer(int x_type, const void *x, const float *dh, int64_t dh_stride, int64_t k, float *da,
-                             const void *dy, const float *h, int64_t rows, const float *scale, float *db, int64_t n,
+hipError_t launch_lora_outer(int x_type, const void *x, const uint16_t *parts_dh, int64_t k, float *da, const void *dy,
+                             const uint16_t *parts_h, int64_t rows, const float *scale, float *db, int64_t n,
                              int64_t rank, int64_t n_adapters, const int32_t *order, const int32_t *bounds, float *part,
                              hipStream_t s) {
     Args a{};
-    a.job[0] = Job{x, dh, da, nullptr, da ? k : 0, dh_stride, 0, 1, 0};
-    a.job[1] = Job{dy, h, db, scale, db ? rows : 0, rank, 0, 0, 0};
+    a.job[0] = Job{x, parts_dh, da, nullptr, da ? k : 0, 0, 1};
+    a.job[1] = Job{dy, parts_h, db, scale, db ? rows : 0, 0, 0};
     a.order = order;
     a.bounds = bounds;
     a.part = part;
+    a.stride = lora_parts_stride(n);
     a.rank = (int32_t)rank;
     a.n_adapters = (int32_t)n_adapters;
     const int rt = rank_tiles(rank);
     int64_t blocks = 0;
     for (Job &j : a.job) {
         j.slices = blocks_of(x_type, rank, j.cols);
-        j.h_vec = rank % rt == 0 && j.h_stride % rt == 0 && (uintptr_t)j.h % (rt * 4 < 16 ? rt * 4 : 16) == 0;
         blocks += j.slices;
     }
     a.splits = splits_of(n, n_adapters, blocks);

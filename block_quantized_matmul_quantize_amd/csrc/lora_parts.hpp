@@ -11,12 +11,11 @@ namespace qmm {
 // ------------------------------------------------------------------------------------------------
 // Rows that share an adapter
 // ------------------------------------------------------------------------------------------------
-// A window is 64 consecutive rows, a lane each.  Rows of one adapter form tiles of up to 32 rows; rows
-// without an adapter (key n_adapters) form tiles of their own, or none.  Found by one ballot per key
-// bit from 256 bytes of ids, so every wave does it for itself: no sort is launched before the forward
-// pass, and a step of single tokens (each row its own adapter) spreads over as many workgroups as it
-// has tiles.
-constexpr int kWindow = 64, kTileRows = 32;
+// A window is 64 consecutive rows, a lane each.  The rows of one adapter in it are a tile; rows without
+// an adapter (key n_adapters) form a tile of their own, or none.  Found by one ballot per key bit from
+// 256 bytes of ids, so every wave does it for itself: no sort is launched before the forward pass, and
+// a step of single tokens (each row its own adapter) spreads over as many workgroups as it has tiles.
+constexpr int kWindow = 64;
 
 struct Tiles {
     int32_t key;    // the lane's row: its adapter
@@ -40,27 +39,28 @@ __device__ __forceinline__ Tiles find_tiles(const int32_t *__restrict__ ids, int
         const uint64_t set = __ballot((t.key >> b) & 1);
         same &= (t.key >> b) & 1 ? set : ~set;
     }
-    const int rank = __popcll(same & ((1ull << lane) - 1)), cnt = __popcll(same);
-    const uint64_t first = __ballot(in && rank == 0), full = __ballot(in && rank == 0 && cnt > kTileRows);
-    const uint64_t below = in ? (1ull << lowest(same)) - 1 : 0;
-    t.tile = in ? __popcll(first & below) + __popcll(full & below) + rank / kTileRows : -1;
-    t.slot = rank % kTileRows;
-    t.count = __popcll(first) + __popcll(full);   // of 64 rows only one adapter can have more than 32
+    t.slot = __popcll(same & ((1ull << lane) - 1));
+    const uint64_t first = __ballot(in && t.slot == 0);
+    t.tile = in ? __popcll(first & ((1ull << lowest(same)) - 1)) : -1;
+    t.count = __popcll(first);
     return t;
 }
 
 struct Tile {
     int32_t key;    // adapter
-    int rows;       // 1 .. 32
+    int rows;       // 1 .. 64
     int at;         // lane l < rows: row of slot l within the window
     __device__ __forceinline__ int row(int slot) const { return __shfl(at, slot < rows ? slot : 0); }
+    // Four waves share a tile: 1, 2 or 4 groups of 16 rows, the waves of a group split the other dimension.
+    __device__ __forceinline__ int groups() const { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
 };
 __device__ __forceinline__ Tile pick_tile(const Tiles &t, int i) {
     const uint64_t m = __ballot(t.tile == i);
     Tile r;
     r.rows = __popcll(m);
     r.key = __builtin_amdgcn_readlane(t.key, lowest(m));
-    // each row's lane number goes to the lane of its slot; the other lanes push to lane 63, which is no slot
+    // each row's lane number goes to the lane of its slot; the other lanes push to lane 63, which is a
+    // slot only where there are no other lanes
     r.at = __builtin_amdgcn_ds_permute((t.tile == i ? t.slot : 63) * 4, (int)(threadIdx.x & 63));
     return r;
 }
@@ -72,15 +72,15 @@ inline int key_bits_of(int64_t n_adapters) {
     return b;
 }
 inline int64_t tiles_of_window(int64_t n, int64_t n_adapters) {
-    const int64_t most = n_adapters + 1 < kWindow ? n_adapters + 2 : kWindow;
+    const int64_t most = n_adapters + 1 < kWindow ? n_adapters + 1 : kWindow;
     return n < most ? n : most;
 }
 // Workgroups that share a window's tiles: one for each tile there can be as long as the launch stays
-// at about 4096 workgroups, else 3 (runs of rows of one request give a window two or three tiles);
-// others of the launch find no tile and end after reading the ids.
+// at about 4096 workgroups, else 2 (runs of rows of one request give a window one or two tiles);
+// those that find no tile end after reading the ids.
 inline int tile_lanes(int64_t others, int64_t n, int64_t n_adapters) {
     const int64_t most = tiles_of_window(n, n_adapters), fit = 4096 / others;
-    const int64_t least = most < 3 ? most : 3;
+    const int64_t least = most < 2 ? most : 2;
     return (int)(fit > most ? most : fit < least ? least : fit);
 }
 // Slices of the other dimension x workgroups of a window x windows (the kernels step through what
@@ -89,6 +89,10 @@ inline dim3 tile_grid(int64_t slices, int lanes, int64_t n) {
     const int64_t windows = (n + kWindow - 1) / kWindow;
     return dim3((unsigned)slices, (unsigned)lanes, (unsigned)(windows < 65535 ? windows : 65535));
 }
+// The slice of a workgroup: turned by one from window to window.  Workgroups go round the eight dies, so
+// with 8 slices each die would otherwise see one range of columns only, and rows a multiple of 4 KB
+// apart would share few of its L2 channels.
+__device__ __forceinline__ int64_t slice_of_block() { return (blockIdx.x + blockIdx.z) % gridDim.x; }
 // Host: calls f(values of the element types of x and of the adapters).
 template <class F> hipError_t with_lora_types(int x_type, int w_type, F f) {
     return with_type(x_type, [&](auto x) -> hipError_t {
