@@ -3,9 +3,10 @@
 //
 // The row matrix v is read once and is nearly all of the traffic (n * k against rank * k weights an
 // adapter, which L2 holds), so HBM bounds the large calls and latency the small ones.  A workgroup
-// takes the rows of one adapter in a window of 64 and a slice of K; its four waves take 16 rows each,
-// or, where there are fewer rows, turns at 32 K values of them, read straight into the operand
-// registers of the matrix instructions: a wave has 16 rows, so there is no reuse that LDS would serve.
+// takes the rows of one adapter in a window of 64 and a slice of K; its four waves take turns at 32 K
+// values of all its rows, read straight into the operand registers of the matrix instructions (nothing
+// is read twice within a workgroup, so LDS would serve no reuse), several steps in flight.  The waves'
+// sums meet in LDS, in a fixed order.
 #include "launch.hpp"
 #include "lora_parts.hpp"
 
@@ -22,23 +23,27 @@ struct Args {
 };
 
 // One 32-value step of K: operands as loaded.
-template <class X, class W, int RT, bool KM> struct Step {
-    Raw8<X> x;
+template <class X, class W, int MT, int RT, bool KM> struct Step {
+    Raw8<X> x[MT];
     typename std::conditional<KM, Raw8<W>, Rows8<W, RT>>::type w[KM ? RT : 1];
 };
 
-template <class X, class W, int RT, bool KM, bool XV, bool WV>
+template <class X, class W, int MT, int RT, bool KM, bool XV, bool WV>
 struct Narrow {
     static constexpr bool kNat = kNative<X, W>;
-    const X *x;             // the lane's row, at its group's first K value
+    typedef Step<X, W, MT, RT, KM> S;
+    const X *x[MT];         // the lane's rows, at its group's first K value
     const W *w;             // KM: m[c], row RT * (lane % 16); else m[c] at column RT * (lane % 16)
     int64_t k, rank;
     int g8, r0;
 
-    template <bool TAIL> __device__ __forceinline__ void load(Step<X, W, RT, KM> &s, int64_t kk) const {
+    template <bool TAIL> __device__ __forceinline__ void load(S &s, int64_t kk) const {
         const int64_t left = k - kk - g8;
-        if constexpr (TAIL) s.x = load8<XV>(x + kk, left);
-        else s.x = load8(x + kk);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            if constexpr (TAIL) s.x[t] = load8<XV>(x[t] + kk, left);
+            else s.x[t] = load8(x[t] + kk);
+        }
         if constexpr (KM) {
 #pragma unroll
             for (int q = 0; q < RT; ++q) {   // ranks past the last repeat it: their sums are not used
@@ -58,37 +63,42 @@ struct Narrow {
             }
         }
     }
-    __device__ __forceinline__ void add(const Step<X, W, RT, KM> &s, f32x4 (&acc)[RT]) const {
-        const auto a = parts_of<kNat>(s.x);
+    __device__ __forceinline__ void add(const S &s, f32x4 (&acc)[MT][RT]) const {
+        decltype(parts_of<kNat>(s.x[0])) a[MT];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) a[t] = parts_of<kNat>(s.x[t]);
 #pragma unroll
         for (int q = 0; q < RT; ++q) {
             Raw8<W> raw;
             if constexpr (KM) raw = s.w[q];
             else raw = s.w[0].column(q);
-            acc[q] = mul_acc<X>(a, parts_of<kNat>(raw), acc[q]);
+            const auto b = parts_of<kNat>(raw);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) acc[t][q] = mul_acc<X>(a[t], b, acc[t][q]);
         }
     }
-    // K values [lo, hi) in steps of 32 at a distance
-    __device__ __forceinline__ void run(int64_t lo, int64_t hi, int distance, f32x4 (&acc)[RT]) const {
-        // steps whose loads are in flight together
-        constexpr int U = RT <= 2 ? 4 : 2;
+    // K values [lo, hi) in steps of 32 at a distance of 128
+    __device__ __forceinline__ void run(int64_t lo, int64_t hi, f32x4 (&acc)[MT][RT]) const {
+        // steps whose loads are in flight together: 8 to 16 KB a wave
+        constexpr int U = RT >= 4 ? (RT == 8 || MT == 4 ? 1 : 2) : MT == 4 ? 2 : 4;
         int64_t kk = lo;
         if constexpr (XV && (WV || !KM)) {
-            for (; kk + distance * (U - 1) + 32 <= hi; kk += distance * U) {
-                Step<X, W, RT, KM> s[U];
+            for (; kk + 128 * (U - 1) + 32 <= hi; kk += 128 * U) {
+                S s[U];
 #pragma unroll
-                for (int u = 0; u < U; ++u) load<false>(s[u], kk + distance * u);
+                for (int u = 0; u < U; ++u) load<false>(s[u], kk + 128 * u);
 #pragma unroll
                 for (int u = 0; u < U; ++u) add(s[u], acc);
             }
-            for (; kk + 32 <= hi; kk += distance) {
-                Step<X, W, RT, KM> s;
-                load<false>(s, kk);
-                add(s, acc);
-            }
+            if constexpr (U > 1)
+                for (; kk + 32 <= hi; kk += 128) {
+                    S s;
+                    load<false>(s, kk);
+                    add(s, acc);
+                }
         }
-        for (; kk < hi; kk += distance) {
-            Step<X, W, RT, KM> s;
+        for (; kk < hi; kk += 128) {
+            S s;
             load<true>(s, kk);
             add(s, acc);
         }
@@ -96,66 +106,64 @@ struct Narrow {
 };
 
 template <class X, class W, int RT, bool KM, bool XV, bool WV>
-__global__ __launch_bounds__(256) void narrow_kernel(Args a) {
+__global__ __launch_bounds__(256, RT == 8 ? 1 : 2) void narrow_kernel(Args a) {
     constexpr int R = 16 * RT;
-    __shared__ alignas(16) float red[3][16][R];
+    __shared__ alignas(16) float red[kWindow][R];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, m = lane & 15, g = lane >> 4;
     const int64_t s = slice_of_block();
     const int64_t lo = s * a.slice, hi = lo + a.slice < a.k ? lo + a.slice : a.k;
-    for (int64_t i0 = (int64_t)blockIdx.z * kWindow; i0 < a.n; i0 += (int64_t)gridDim.z * kWindow) {
+    for (int64_t i0 = (int64_t)blockIdx.y * kWindow; i0 < a.n; i0 += (int64_t)gridDim.y * kWindow) {
         const Tiles tiles = find_tiles(a.ids, i0, a.n, a.n_adapters, a.key_bits, false);
-        for (int i = blockIdx.y; i < tiles.count; i += gridDim.y) {
+        for (int i = blockIdx.z; i < tiles.count; i += gridDim.z) {
             const Tile t = pick_tile(tiles, i);
-            const int groups = t.groups(), slot0 = 16 * (wave % groups), turn = wave / groups, turns = 4 / groups;
-            Narrow<X, W, RT, KM, XV, WV> op;
-            op.k = a.k;
-            op.rank = a.rank;
-            op.g8 = 8 * g;
-            op.r0 = RT * m < a.rank ? RT * m : a.rank - 1;
-            if (WV && !KM && op.r0 + RT > a.rank) op.r0 = a.rank - RT;
-            op.x = (const X *)a.v + (i0 + t.row(slot0 + m)) * a.k + op.g8;
-            op.w = (const W *)a.m + (int64_t)t.key * a.rank * a.k + (KM ? op.r0 * a.k : op.r0);
-            f32x4 acc[RT];
+            with_groups(t, [&](auto groups) {
+                constexpr int MT = decltype(groups)::value;
+                Narrow<X, W, MT, RT, KM, XV, WV> op;
+                op.k = a.k;
+                op.rank = a.rank;
+                op.g8 = 8 * g;
+                op.r0 = RT * m < a.rank ? RT * m : a.rank - 1;
+                if (WV && !KM && op.r0 + RT > a.rank) op.r0 = a.rank - RT;
 #pragma unroll
-            for (int q = 0; q < RT; ++q) acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if (slot0 < t.rows) op.run(lo + 32 * turn, hi, 32 * turns, acc);
-            if (turns > 1) {   // the waves of a group meet in LDS, in a fixed order
-                if (turn > 0)
+                for (int u = 0; u < MT; ++u) op.x[u] = (const X *)a.v + (i0 + t.row(16 * u + m)) * a.k + op.g8;
+                op.w = (const W *)a.m + (int64_t)t.key * a.rank * a.k + (KM ? op.r0 * a.k : op.r0);
+                f32x4 acc[MT][RT];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
+                for (int u = 0; u < MT; ++u)
 #pragma unroll
-                        for (int q = 0; q < RT; ++q) red[wave - groups][4 * g + e][RT * m + q] = acc[q][e];
-                __syncthreads();
-                if (turn == 0)
-                    for (int w = groups; w < 4; w += groups)
+                    for (int q = 0; q < RT; ++q) acc[u][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+                op.run(lo + 32 * wave, hi, acc);
+#pragma unroll 1
+                for (int w = 0; w < 4; ++w) {
+                    if (w == wave)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
+                        for (int u = 0; u < MT; ++u)
 #pragma unroll
-                            for (int q = 0; q < RT; ++q) acc[q][e] += red[w - groups + wave][4 * g + e][RT * m + q];
-                __syncthreads();
-            }
+                            for (int e = 0; e < 4; ++e)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int slot = slot0 + 4 * g + e;
-                const int64_t row = i0 + t.row(slot);
-                if (turn == 0 && slot < t.rows) {
-                    Piece<float, RT> o;
-#pragma unroll
-                    for (int q = 0; q < RT; ++q) o.v[q] = acc[q][e];
-                    *(Piece<float, RT> *)(a.part + (s * a.n + row) * R + RT * m) = o;
+                                for (int q = 0; q < RT; ++q) {
+                                    float *p = &red[16 * u + 4 * g + e][RT * m + q];
+                                    *p = w ? *p + acc[u][q][e] : acc[u][q][e];
+                                }
+                    __syncthreads();
                 }
+            });
+            for (int j0 = 0; j0 < t.rows * (R / 4); j0 += 256) {
+                const int j = j0 + threadIdx.x, slot = j / (R / 4), r = j % (R / 4) * 4;
+                const int64_t row = i0 + t.row(slot);   // every lane takes part in the exchange
+                if (slot < t.rows) *(f32x4 *)(a.part + (s * a.n + row) * R + r) = *(const f32x4 *)&red[slot][r];
             }
+            __syncthreads();
         }
     }
 }
 
 int tiles_of_rank(int64_t rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
 
-// Slices of K: enough for two waves of 16 rows on each of the 1024 SIMD units, at most 16 partial sums
-// a result, each of 128 values or more.
+// Slices of K: enough for 256 workgroups, at most 16 partial sums a result, each of 128 values or more.
 int slices_of(int64_t n, int64_t k) {
-    const int64_t steps = (k + 127) / 128, groups = (n + 15) / 16;
-    int64_t s = 2048 / groups;
+    const int64_t steps = (k + 127) / 128, windows = (n + kWindow - 1) / kWindow;
+    int64_t s = 256 / windows;
     if (s > 16) s = 16;
     if (s > steps) s = steps;
     return s < 1 ? 1 : (int)s;

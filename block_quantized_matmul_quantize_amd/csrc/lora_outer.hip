@@ -58,23 +58,28 @@ __global__ __launch_bounds__(256) void outer_kernel(Args a) {
         for (int p = 0; p < RT; ++p)
 #pragma unroll
             for (int q = 0; q < V; ++q) acc[p][q] = f32x4{0.f, 0.f, 0.f, 0.f};
-        const int64_t step = (int64_t)a.splits * 4 * 32;
         // steps at multiples of 32 places; an adapter without rows has none (its lo may be past the last row)
-        for (int64_t p0 = lo < hi ? lo / 32 * 32 + (split * 4 + wave) * 32 : hi; p0 < hi; p0 += step) {
+        const int64_t step = (int64_t)a.splits * 4 * 32;
+        const int64_t start = lo < hi ? lo / 32 * 32 + (split * 4 + wave) * 32 : hi;
+        auto rows_of = [&](int64_t p0) {   // lane l: row of place p0 + l % 32 (of a place of the adapter, at the ends)
             const int64_t at = p0 + (lane & 31);
-            const int32_t idx = a.order[at < lo ? lo : at < hi ? at : hi - 1];
+            return a.order[at < lo ? lo : at < hi ? at : hi - 1];
+        };
+        int32_t rows = start < hi ? rows_of(start) : 0;
+        for (int64_t p0 = start; p0 < hi; p0 += step) {
             Rows8<X, V> xs;
             Frag<3> hf[RT];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int64_t i = __shfl(rows, 8 * g + e);
+                xs.row[e] = load_row<VV, V>(v + i * job.cols + col, nc);
+            }
+            rows = rows_of(p0 + step);   // the next step's, in flight during this one
 #pragma unroll
             for (int p = 0; p < RT; ++p)
 #pragma unroll
                 for (int j = 0; j < 3; ++j)
                     hf[p].p[j] = *(const u32x4 *)(job.h + (j * R + 16 * p + m) * a.stride + p0 + 8 * g);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int64_t i = __shfl(idx, 8 * g + e);
-                xs.row[e] = load_row<VV, V>(v + i * job.cols + col, nc);
-            }
             if (p0 < lo || p0 + 32 > hi) {   // places of other adapters
                 u32x4 keep;
 #pragma unroll
@@ -145,10 +150,10 @@ __global__ __launch_bounds__(256) void join_kernel(const float *__restrict__ par
 
 
 
-// Workgroups an adapter's rows are split over: 512 in all, while each wave keeps two steps of the
+// Workgroups an adapter's rows are split over: 256 in all, while each wave keeps two steps of the
 // average adapter's rows.
 int splits_of(int64_t n, int64_t n_adapters, int64_t blocks) {
-    int64_t s = 512 / (blocks * n_adapters), most = n / n_adapters / 256;
+    int64_t s = 256 / (blocks * n_adapters), most = n / n_adapters / 256;
     if (s > most) s = most;
     return s < 1 ? 1 : s > 16 ? 16 : (int)s;
 }

@@ -3,12 +3,12 @@
 // rows without an adapter get base, or zeros.
 //
 // It reads base and writes out, 8 bytes an fp32 result, against a few operations for each: HBM bounds
-// it.  A workgroup takes the rows of one adapter in a window of 64 and a slice of the columns; each of
-// its four waves 16 rows, or, where there are fewer, its share of the columns.  A wave adds up the
-// slices of its rows' h and keeps their bf16 parts in registers for all its columns.  Lane l % 16 owns
-// four neighbouring columns of a row, so that base is read and out written 256 (fp32) or 128 bytes a
-// row at a time, straight from the accumulators: column q of the lanes' pieces is one matrix
-// instruction's 16 columns.  No wave waits for another.
+// it.  A workgroup takes the rows of one adapter in a window of 64 and a slice of the columns; it adds
+// up the slices of its rows' h and leaves their bf16 parts in LDS.  A wave takes 64 columns at a time for
+// all the rows: it loads the adapter's part for them once, and holds base for 64 rows (16 KB) in flight.
+// Lane l % 16 owns four neighbouring columns of a row, so that base is read and out written 256 (fp32)
+// or 128 bytes a row at a time, straight from the accumulators: column q of the lanes' pieces is one
+// matrix instruction's 16 columns.
 #include "launch.hpp"
 #include "lora_parts.hpp"
 
@@ -28,126 +28,160 @@ struct Args {
     int32_t n_adapters, key_bits, rank, padded, parts, slices, lanes;
 };
 
+template <int R> struct Stage {
+    uint16_t v[3][kWindow][R + 8];   // keeps 16-byte pieces, and rows off the same banks
+    __device__ __forceinline__ void put(int slot, int r, const float (&x)[4]) {
+        uint32_t p[3][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float mid = rest_of(x[i]);
+            p[0][i] = __float_as_uint(x[i]);
+            p[1][i] = __float_as_uint(mid);
+            p[2][i] = __float_as_uint(mid - __uint_as_float(p[1][i] & 0xffff0000u));
+        }
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+            *(u32x2 *)&v[j][slot][r] = u32x2{high_halves(p[j][0], p[j][1]), high_halves(p[j][2], p[j][3])};
+    }
+    __device__ __forceinline__ Frag<3> get(int slot, int r) const {
+        Frag<3> f;
+#pragma unroll
+        for (int p = 0; p < 3; ++p) f.p[p] = *(const u32x4 *)&v[p][slot][r];
+        return f;
+    }
+};
+
 template <class X, class W, int KS, bool KM, bool OV, bool WV>
-__global__ __launch_bounds__(256, KS == 1 ? 4 : KS == 2 ? 3 : 2) void wide_kernel(Args a) {
+__global__ __launch_bounds__(256, KS == 4 ? 1 : 2) void wide_kernel(Args a) {
     constexpr int R = 32 * KS;                        // K of the product
     constexpr int V = kPiece;
+    __shared__ alignas(16) Stage<R> stage;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, m = lane & 15, g = lane >> 4;
     const int64_t slice = slice_of_block();
     const int64_t lo = slice * a.slice, hi = lo + a.slice < a.cols ? lo + a.slice : a.cols;
-    for (int64_t i0 = (int64_t)blockIdx.z * kWindow; i0 < a.n; i0 += (int64_t)gridDim.z * kWindow) {
+    for (int64_t i0 = (int64_t)blockIdx.y * kWindow; i0 < a.n; i0 += (int64_t)gridDim.y * kWindow) {
         const Tiles tiles = find_tiles(a.ids, i0, a.n, a.n_adapters, a.key_bits, true);
-        for (int i = blockIdx.y; i < tiles.count; i += gridDim.y) {
+        for (int i = blockIdx.z; i < tiles.count; i += gridDim.z) {
             const Tile t = pick_tile(tiles, i);
             const bool some = t.key < a.n_adapters;
-            const int groups = t.groups(), slot0 = 16 * (wave % groups), turns = 4 / groups;
-            int64_t c0 = lo + wave / groups * (16 * V);
-            if (slot0 >= t.rows || c0 >= hi) continue;
-            int64_t row[4];
-            bool live[4];
+            with_groups(t, [&](auto groups) {
+                constexpr int MT = decltype(groups)::value;
+                const X *base = (const X *)a.base;
+                const W *w = (const W *)a.m + (int64_t)t.key * a.rank * a.cols;
+                int32_t row[MT][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int slot = slot0 + 4 * g + e;
-                live[e] = slot < t.rows;
-                row[e] = (i0 + t.row(slot)) * a.cols;   // slots past the last: row of slot 0, not stored
-            }
-            const X *base = (const X *)a.base;
-            const W *w = (const W *)a.m + (int64_t)t.key * a.rank * a.cols;
-            // a lane's columns: all V, or some, or none at the end (nothing of those is stored)
-            auto col_of = [&](int64_t at) { return at + V * m < hi ? at + V * m : OV ? hi - V : hi - 1; };
-            auto width_of = [&](int64_t col) { return OV || hi - col >= V ? V : (int)(hi - col); };
-            Piece<X, V> b[4];
-            auto load_base = [&](int64_t at) {
-                const int64_t col = col_of(at);
+                for (int u = 0; u < MT; ++u)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) b[e] = load_row<OV, V>(base + row[e] + col, width_of(col));
-            };
-            if (base) load_base(c0);
-            Frag<3> h[KS];
-            if (some) {
-                const float c = a.scale ? a.scale[t.key] : 1.f;
-                const float *p = a.part + (i0 + t.row(slot0 + m)) * a.padded;
-                const int64_t next = a.n * a.padded;
+                    for (int e = 0; e < 4; ++e)   // slots past the last: row of slot 0, not stored
+                        row[u][e] = (int32_t)i0 + t.row(16 * u + 4 * g + e);
+                // a lane's columns: all V, or some, or none at the end (nothing of those is stored)
+                auto col_of = [&](int64_t at) { return at + V * m < hi ? at + V * m : OV ? hi - V : hi - 1; };
+                auto width_of = [&](int64_t col) { return OV || hi - col >= V ? V : (int)(hi - col); };
+                Piece<X, V> b[MT][4];
+                auto load_base = [&](int64_t at) {
+                    const int64_t col = col_of(at);
 #pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    const int r0 = 32 * s + 8 * g;
-                    const float *q = p + (r0 < a.padded ? r0 : 0);
-                    f32x4 u0 = *(const f32x4 *)q, u1 = *(const f32x4 *)(q + 4);
-#pragma unroll 4
-                    for (int i = 1; i < a.parts; ++i) {
-                        u0 += *(const f32x4 *)(q + i * next);
-                        u1 += *(const f32x4 *)(q + i * next + 4);
-                    }
-                    float v[8];
+                    for (int u = 0; u < MT; ++u)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)   // ranks past the last hold nothing of use
-                        v[e] = r0 + e < a.rank ? (e < 4 ? u0[e & 3] : u1[e & 3]) * c : 0.f;
-                    h[s] = split8<3>(v);
-                }
-            }
-            for (; c0 < hi; c0 += turns * 16 * V) {
-                const int64_t col = col_of(c0);
-                const int nw = width_of(col);
-                f32x4 acc[V];
-#pragma unroll
-                for (int q = 0; q < V; ++q) acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+                        for (int e = 0; e < 4; ++e) b[u][e] = load_row<OV, V>(base + row[u][e] * a.cols + col, width_of(col));
+                };
+                int64_t c0 = lo + wave * (16 * V);
+                if (base && c0 < hi) load_base(c0);
                 if (some) {
+                    const float c = a.scale ? a.scale[t.key] : 1.f;
+                    const int64_t next = a.n * a.padded;
 #pragma unroll
-                    for (int s = 0; s < KS; ++s) {
-                        const int r0 = 32 * s + 8 * g;
-                        Raw8<W> raw[V];
-                        if constexpr (KM) {
+                    for (int u = 0; u < MT * KS / 2 || u == 0; ++u) {
+                        const int j = 256 * u + threadIdx.x, slot = j / (R / 4), r = j % (R / 4) * 4;
+                        const float *p = a.part + (i0 + t.row(slot)) * a.padded + (r < a.padded ? r : 0);
+                        f32x4 sum = *(const f32x4 *)p;
+#pragma unroll 4
+                        for (int s = 1; s < a.parts; ++s) sum += *(const f32x4 *)(p + s * next);
+                        float v[4];
 #pragma unroll
-                            for (int q = 0; q < V; ++q) {
-                                const W *p = w + (col + (OV || q < nw ? q : nw - 1)) * a.rank;
-                                if constexpr (WV) raw[q] = load8(p + (r0 < a.rank ? r0 : 0));
-                                else raw[q] = load8<false>(p + r0, a.rank - r0);
-                            }
-                            if (WV && a.rank < R && r0 >= a.rank)
+                        for (int q = 0; q < 4; ++q) v[q] = r + q < a.rank ? sum[q] * c : 0.f;   // no other rank is of use
+                        stage.put(slot, r, v);
+                    }
+                    __syncthreads();
+                }
+                for (; c0 < hi; c0 += 64 * V) {
+                    const int64_t col = col_of(c0);
+                    const int nw = width_of(col);
+                    f32x4 acc[MT][V];
 #pragma unroll
-                                for (int q = 0; q < V; ++q) raw[q] = Raw8<W>{};
-                        } else {
-                            Rows8<W, V> rows;
+                    for (int u = 0; u < MT; ++u)
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                rows.row[e] = load_row<OV, V>(w + (r0 + e < a.rank ? r0 + e : 0) * a.cols + col, nw);
-                            if (a.rank < R)
+                        for (int q = 0; q < V; ++q) acc[u][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    if (some) {
+#pragma unroll
+                        for (int s = 0; s < KS; ++s) {
+                            const int r0 = 32 * s + 8 * g;
+                            Raw8<W> raw[V];
+                            if constexpr (KM) {
+#pragma unroll
+                                for (int q = 0; q < V; ++q) {
+                                    const W *p = w + (col + (OV || q < nw ? q : nw - 1)) * a.rank;
+                                    if constexpr (WV) raw[q] = load8(p + (r0 < a.rank ? r0 : 0));
+                                    else raw[q] = load8<false>(p + r0, a.rank - r0);
+                                }
+                                if (WV && a.rank < R && r0 >= a.rank)
+#pragma unroll
+                                    for (int q = 0; q < V; ++q) raw[q] = Raw8<W>{};
+                            } else {
+                                Rows8<W, V> rows;
 #pragma unroll
                                 for (int e = 0; e < 8; ++e)
-                                    if (r0 + e >= a.rank)
+                                    rows.row[e] = load_row<OV, V>(w + (r0 + e < a.rank ? r0 + e : 0) * a.cols + col, nw);
+                                if (a.rank < R)
 #pragma unroll
-                                        for (int q = 0; q < V; ++q) rows.row[e].v[q] = (W)0.f;
+                                    for (int e = 0; e < 8; ++e)
+                                        if (r0 + e >= a.rank)
 #pragma unroll
-                            for (int q = 0; q < V; ++q) raw[q] = rows.column(q);
+                                            for (int q = 0; q < V; ++q) rows.row[e].v[q] = (W)0.f;
+#pragma unroll
+                                for (int q = 0; q < V; ++q) raw[q] = rows.column(q);
+                            }
+                            decltype(parts_of<false>(raw[0])) f[V];
+#pragma unroll
+                            for (int q = 0; q < V; ++q) f[q] = parts_of<false>(raw[q]);
+#pragma unroll
+                            for (int u = 0; u < MT; ++u) {
+                                const Frag<3> h = stage.get(16 * u + m, r0);
+#pragma unroll
+                                for (int q = 0; q < V; ++q) acc[u][q] = mul_acc<bf16_t>(h, f[q], acc[u][q]);
+                            }
                         }
-#pragma unroll
-                        for (int q = 0; q < V; ++q) acc[q] = mul_acc<bf16_t>(h[s], parts_of<false>(raw[q]), acc[q]);
                     }
+                    if (base)
+#pragma unroll
+                        for (int u = 0; u < MT; ++u)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                                for (int q = 0; q < V; ++q) acc[u][q][e] = (float)b[u][e].v[q] + acc[u][q][e];
+                    const bool in = c0 + V * m < hi;
+                    const int64_t at = c0 + 64 * V;
+                    if (base && at < hi) load_base(at);
+#pragma unroll
+                    for (int u = 0; u < MT; ++u)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (16 * u + 4 * g + e >= t.rows || !in) continue;
+                            Piece<X, V> o;
+#pragma unroll
+                            for (int q = 0; q < V; ++q) o.v[q] = (X)acc[u][q][e];
+                            X *p = (X *)a.out + row[u][e] * a.cols + col;
+                            if constexpr (OV) {
+                                *(Piece<X, V> *)p = o;
+                            } else {
+#pragma unroll
+                                for (int q = 0; q < V; ++q)
+                                    if (q < nw) p[q] = o.v[q];
+                            }
+                        }
                 }
-                if (base)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-#pragma unroll
-                        for (int q = 0; q < V; ++q) acc[q][e] = (float)b[e].v[q] + acc[q][e];
-                const bool in = c0 + V * m < hi;
-                const int64_t at = c0 + turns * 16 * V;
-                if (base && at < hi) load_base(at);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (!live[e] || !in) continue;
-                    Piece<X, V> o;
-#pragma unroll
-                    for (int q = 0; q < V; ++q) o.v[q] = (X)acc[q][e];
-                    X *p = (X *)a.out + row[e] + col;
-                    if constexpr (OV) {
-                        *(Piece<X, V> *)p = o;
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < V; ++q)
-                            if (q < nw) p[q] = o.v[q];
-                    }
-                }
-            }
+                if (some) __syncthreads();
+            });
         }
     }
 }
@@ -189,9 +223,9 @@ hipError_t launch_lora_wide(int x_type, int w_type, bool by_row, const float *pa
     a.base = base;
     a.out = out;
     const int64_t windows = (n + kWindow - 1) / kWindow;
-    // columns of a workgroup: 4 steps of 16 pieces, or 8 or 16 as long as there are 1024 workgroups
+    // columns of a workgroup: one step of its four waves, or 2 or 4 as long as there are 512 workgroups
     a.slice = 64 * kPiece;
-    while (a.slice < 256 * kPiece && windows * ((cols + 2 * a.slice - 1) / (2 * a.slice)) >= 1024) a.slice *= 2;
+    while (a.slice < 256 * kPiece && windows * ((cols + 2 * a.slice - 1) / (2 * a.slice)) >= 512) a.slice *= 2;
     a.slices = (int32_t)((cols + a.slice - 1) / a.slice);
     a.lanes = tile_lanes(windows * a.slices, n, n_adapters);
     return with_lora_types(x_type, w_type, [&](auto x, auto w) -> hipError_t {
