@@ -4,12 +4,14 @@
 //
 // A least-significant-digit radix sort with digits of up to 11 bits: n_keys + 1 key values of up to
 // 11 bits (any expert or adapter count) are one pass, a vocabulary of 2^18 two.  In a pass, each
-// workgroup owns a contiguous chunk and each of its waves a contiguous part of that:
-//   1. count: one digit histogram per chunk (skipped when one workgroup holds everything);
-//   2. scatter: a workgroup adds up the chunks' histograms for the digits' first places and its own
-//      chunk's offset in them, counts per wave, and places 64 elements at a time: lanes with equal
-//      digits find each other by one ballot per digit bit, a lane's rank is the number of such lanes
-//      below it.  No atomic decides an order, so the result is the stable one, always.
+// workgroup owns a contiguous chunk and each of its waves a contiguous part of that.  It needs the
+// digits' counts over all chunks and over those before its own:
+//   - up to kFused elements each workgroup counts all of them itself, so that a pass is one launch (the
+//     ids, 256 KB at most, come from L2; counting them all again costs less than a launch);
+//   - beyond, a launch before leaves one histogram per chunk.
+// Then it counts per wave and places 64 elements at a time: lanes with equal digits find each other by
+// one ballot per digit bit, a lane's rank is the number of such lanes below it.  No atomic decides an
+// order, so the result is the stable one, always.
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -19,7 +21,8 @@ namespace {
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kMaxBits = 11;
-constexpr int64_t kOneGroup = 16384;    // elements that one workgroup sorts in a launch of its own
+constexpr int64_t kFused = 65536;       // elements that every workgroup counts itself
+constexpr int64_t kFusedChunk = 1024;   // and those it places: one step of its 16 waves
 constexpr int64_t kMaxChunks = 128;
 
 __device__ __forceinline__ int32_t key_of(const int32_t *ids, int64_t i, int32_t n_keys) {
@@ -30,14 +33,45 @@ __device__ __forceinline__ int32_t key_of(const int32_t *ids, int64_t i, int32_t
 struct Pass {
     const int32_t *ids;
     const int32_t *src;     // element order before this pass; null: 0, 1, 2, ...
+    const int32_t *keys;    // keys in that order; null: those of ids
     int32_t *dst;           // element order after it
     int32_t *pos;           // last pass: each index's place, -1 for an id out of range
-    int32_t *skeys;         // last pass, or null: the keys in order
+    int32_t *skeys;         // or null: the keys in the order after it
     int32_t *bounds;        // only pass, or null: first place of each key
-    int32_t *table;         // [chunks][digits] histograms (more than one chunk)
+    int32_t *table;         // [chunks][digits] histograms, or null: counted here
     int64_t n, chunk;
     int32_t n_keys, shift, bits;
 };
+
+__device__ __forceinline__ int32_t digit_of(const Pass &p, int64_t i) {
+    const int32_t key = p.keys ? p.keys[i] : key_of(p.ids, i, p.n_keys);
+    return (key >> p.shift) & ((1 << p.bits) - 1);
+}
+
+// hist[digit] += number of elements of [lo, hi), by all threads, four elements a thread in flight.
+// Where a whole wave has one digit (runs of one id) one lane adds for all.
+__device__ __forceinline__ void count(const Pass &p, int64_t lo, int64_t hi, int32_t *hist) {
+    auto add = [&](int32_t d, bool in) {
+        const uint64_t m = __ballot(in);
+        if (m == 0) return;
+        const int32_t d0 = __builtin_amdgcn_readlane(d, __ffsll((unsigned long long)m) - 1);
+        if (__ballot(in && d != d0) == 0) {
+            if ((threadIdx.x & 63) == 0) atomicAdd(&hist[d0], __popcll(m));
+        } else if (in) {
+            atomicAdd(&hist[d], 1);
+        }
+    };
+    for (int64_t i0 = lo; i0 < hi; i0 += 4 * kThreads) {
+        int32_t d[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t i = i0 + u * kThreads + threadIdx.x;
+            d[u] = digit_of(p, i < hi ? i : lo);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) add(d[u], i0 + u * kThreads + threadIdx.x < hi);
+    }
+}
 
 __global__ __launch_bounds__(kThreads) void count_kernel(Pass p) {
     extern __shared__ int32_t hist[];
@@ -45,10 +79,7 @@ __global__ __launch_bounds__(kThreads) void count_kernel(Pass p) {
     for (int d = threadIdx.x; d < D; d += kThreads) hist[d] = 0;
     __syncthreads();
     const int64_t lo = blockIdx.x * p.chunk, hi = lo + p.chunk < p.n ? lo + p.chunk : p.n;
-    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
-        const int32_t key = key_of(p.ids, p.src ? p.src[i] : i, p.n_keys);
-        atomicAdd(&hist[(key >> p.shift) & (D - 1)], 1);
-    }
+    count(p, lo, hi, hist);
     __syncthreads();
     for (int d = threadIdx.x; d < D; d += kThreads) p.table[(int64_t)blockIdx.x * D + d] = hist[d];
 }
@@ -72,21 +103,24 @@ __device__ __forceinline__ int32_t scan_threads(int32_t v, int32_t *wsum) {
 }
 
 __global__ __launch_bounds__(kThreads) void scatter_kernel(Pass p) {
-    extern __shared__ int32_t hist[];   // [wave][digit]: counts, then the next place
+    extern __shared__ int32_t hist[];   // [wave][digit]: counts, then the next place; [before, after][digit]
     __shared__ int32_t wsum[kWaves];
     const int D = 1 << p.bits;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int i = threadIdx.x; i < kWaves * D; i += kThreads) hist[i] = 0;
+    const bool others = !p.table && gridDim.x > 1;
+    for (int i = threadIdx.x; i < (kWaves + (others ? 2 : 0)) * D; i += kThreads) hist[i] = 0;
     __syncthreads();
+    if (others) {
+        const int64_t lo = blockIdx.x * p.chunk, hi = lo + p.chunk;
+        count(p, 0, lo, hist + kWaves * D);
+        if (hi < p.n) count(p, hi, p.n, hist + (kWaves + 1) * D);
+    }
     // contiguous part of the chunk for each wave, a multiple of 64 elements
     const int64_t part = p.chunk / kWaves;
     const int64_t lo0 = blockIdx.x * p.chunk + wave * part;
     const int64_t lo = lo0 < p.n ? lo0 : p.n, hi = lo + part < p.n ? lo + part : p.n;
     int32_t *mine = hist + wave * D;
-    for (int64_t i = lo + lane; i < hi; i += 64) {
-        const int32_t key = key_of(p.ids, p.src ? p.src[i] : i, p.n_keys);
-        atomicAdd(&mine[(key >> p.shift) & (D - 1)], 1);
-    }
+    for (int64_t i = lo + lane; i < hi; i += 64) atomicAdd(&mine[digit_of(p, i)], 1);
     __syncthreads();
     // first place of each digit: thread t owns digits [t * per, (t + 1) * per)
     const int per = (D + kThreads - 1) / kThreads;
@@ -97,8 +131,12 @@ __global__ __launch_bounds__(kThreads) void scatter_kernel(Pass p) {
         const int d = threadIdx.x * per + j;
         total[j] = before[j] = 0;
         if (j < per && d < D) {
-            if (chunks == 1) {
+            if (!p.table) {
                 for (int w = 0; w < kWaves; ++w) total[j] += hist[w * D + d];
+                if (others) {
+                    before[j] = hist[kWaves * D + d];
+                    total[j] += before[j] + hist[(kWaves + 1) * D + d];
+                }
             } else {
                 for (int c = 0; c < chunks; ++c) {
                     const int32_t v = p.table[(int64_t)c * D + d];
@@ -129,7 +167,7 @@ __global__ __launch_bounds__(kThreads) void scatter_kernel(Pass p) {
         const int64_t i = i0 + lane;
         const bool in = i < hi;
         const int32_t e = in ? (p.src ? p.src[i] : (int32_t)i) : 0;
-        const int32_t key = in ? key_of(p.ids, e, p.n_keys) : 0;
+        const int32_t key = in ? (p.keys ? p.keys[i] : key_of(p.ids, i, p.n_keys)) : 0;
         const int32_t d = (key >> p.shift) & (D - 1);
         uint64_t same = __ballot(in);
         for (int b = 0; b < p.bits; ++b) {
@@ -170,7 +208,7 @@ __global__ __launch_bounds__(256) void bounds_kernel(const int32_t *__restrict__
 struct Layout {
     int bits, passes;
     int64_t chunk, chunks;
-    size_t table, tmp[2], skeys, total;
+    size_t table, tmp[2], keys[2], skeys, total;   // keys: of the passes before the last
 };
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -181,20 +219,20 @@ Layout layout(int64_t n, int64_t n_keys, bool skeys) {
     while ((n_keys >> bits) != 0) ++bits;
     L.passes = (bits + kMaxBits - 1) / kMaxBits;
     L.bits = (bits + L.passes - 1) / L.passes;
-    if (n <= kOneGroup) {
-        L.chunk = kOneGroup;
-        L.chunks = 1;
+    if (n <= kFused) {
+        L.chunk = kFusedChunk;
     } else {
-        int64_t c = (n + kMaxChunks - 1) / kMaxChunks;
-        if (c < 2048) c = 2048;
+        const int64_t c = (n + kMaxChunks - 1) / kMaxChunks;
         L.chunk = (c + kThreads - 1) / kThreads * kThreads;
-        L.chunks = (n + L.chunk - 1) / L.chunk;
     }
+    L.chunks = n > 0 ? (n + L.chunk - 1) / L.chunk : 1;
     size_t off = 0;
     L.table = off;
-    if (L.chunks > 1) off += up256((size_t)L.chunks * ((size_t)4 << L.bits));
+    if (n > kFused) off += up256((size_t)L.chunks * ((size_t)4 << L.bits));
     for (int i = 0; i < 2; ++i) {
         L.tmp[i] = off;
+        if (L.passes > 1 + i) off += up256((size_t)n * 4);
+        L.keys[i] = off;
         if (L.passes > 1 + i) off += up256((size_t)n * 4);
     }
     L.skeys = off;
@@ -220,20 +258,21 @@ hipError_t launch_sort_ids(const int32_t *ids, int64_t n, int64_t n_keys, int32_
     p.n_keys = (int32_t)n_keys;
     p.chunk = L.chunk;
     p.bits = L.bits;
-    p.table = (int32_t *)(ws + L.table);
+    p.table = n > kFused ? (int32_t *)(ws + L.table) : nullptr;
     int32_t *skeys = with_keys || L.passes > 1 ? (int32_t *)(ws + L.skeys) : nullptr;
     for (int i = 0; i < L.passes; ++i) {
         const bool last = i + 1 == L.passes;
         p.shift = i * L.bits;
-        p.src = i == 0 ? nullptr : (const int32_t *)(ws + L.tmp[(i - 1) & 1]);
+        p.src = i == 0 ? nullptr : p.dst;
+        p.keys = i == 0 ? nullptr : p.skeys;
         p.dst = last ? order : (int32_t *)(ws + L.tmp[i & 1]);
+        p.skeys = last ? skeys : (int32_t *)(ws + L.keys[i & 1]);
         p.pos = last ? pos : nullptr;
-        p.skeys = last ? skeys : nullptr;
         p.bounds = L.passes == 1 ? bounds : nullptr;
-        if (L.chunks > 1)
+        if (p.table)
             hipLaunchKernelGGL(count_kernel, dim3((unsigned)L.chunks), dim3(kThreads), (size_t)4 << L.bits, s, p);
-        hipLaunchKernelGGL(scatter_kernel, dim3((unsigned)L.chunks), dim3(kThreads), (size_t)(4 * kWaves) << L.bits, s,
-                           p);
+        hipLaunchKernelGGL(scatter_kernel, dim3((unsigned)L.chunks), dim3(kThreads),
+                           (size_t)(4 * (kWaves + 2)) << L.bits, s, p);
     }
     if (bounds && L.passes > 1)
         hipLaunchKernelGGL(bounds_kernel, dim3((unsigned)((n_keys + 256) / 256)), dim3(256), 0, s, skeys, n, n_keys,
