@@ -43,17 +43,22 @@ struct Pass {
     int32_t n_keys, shift, bits;
 };
 
-__device__ __forceinline__ int32_t digit_of(const Pass &p, int64_t i) {
-    const int32_t key = p.keys ? p.keys[i] : key_of(p.ids, i, p.n_keys);
+__device__ __forceinline__ int32_t digit_of_key(const Pass &p, int32_t key) {
     return (key >> p.shift) & ((1 << p.bits) - 1);
 }
+__device__ __forceinline__ int32_t digit_of(const Pass &p, int64_t i) {
+    return digit_of_key(p, p.keys ? p.keys[i] : key_of(p.ids, i, p.n_keys));
+}
 
-// hist[digit] += number of elements of [lo, hi), by all threads, four elements a thread in flight.
+// hist[digit] += number of elements of [lo, hi), by all threads, sixteen elements a thread in flight.
 // Where a whole wave has one digit (runs of one id) one lane adds for all.
 __device__ __forceinline__ void count(const Pass &p, int64_t lo, int64_t hi, int32_t *hist) {
-    auto add = [&](int32_t d, bool in) {
+    typedef i32x4 __attribute__((aligned(4))) i32x4_a4;
+    const int32_t *src = p.keys ? p.keys : p.ids;
+    auto add = [&](int32_t v, bool in) {
         const uint64_t m = __ballot(in);
         if (m == 0) return;
+        const int32_t d = digit_of_key(p, (uint32_t)v < (uint32_t)p.n_keys ? v : p.n_keys);
         const int32_t d0 = __builtin_amdgcn_readlane(d, __ffsll((unsigned long long)m) - 1);
         if (__ballot(in && d != d0) == 0) {
             if ((threadIdx.x & 63) == 0) atomicAdd(&hist[d0], __popcll(m));
@@ -61,15 +66,24 @@ __device__ __forceinline__ void count(const Pass &p, int64_t lo, int64_t hi, int
             atomicAdd(&hist[d], 1);
         }
     };
-    for (int64_t i0 = lo; i0 < hi; i0 += 4 * kThreads) {
-        int32_t d[4];
+    int64_t i0 = lo;
+    for (; i0 + 4 * kThreads <= hi; i0 += 16 * kThreads) {
+        i32x4 v[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int64_t i = i0 + u * kThreads + threadIdx.x;
-            d[u] = digit_of(p, i < hi ? i : lo);
+            const int64_t at = i0 + u * 4 * kThreads;
+            v[u] = *(const i32x4_a4 *)(src + (at + 4 * kThreads <= hi ? at : i0) + 4 * threadIdx.x);
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) add(d[u], i0 + u * kThreads + threadIdx.x < hi);
+        for (int u = 0; u < 4; ++u)
+            if (i0 + (u + 1) * 4 * kThreads <= hi)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) add(v[u][q], true);
+    }
+    const int64_t done = lo + (hi - lo) / (4 * kThreads) * (4 * kThreads);
+    for (int u = 0; u < 4; ++u) {
+        const int64_t i = done + u * kThreads + threadIdx.x;
+        if (done + u * kThreads < hi) add(src[i < hi ? i : done], i < hi);
     }
 }
 
