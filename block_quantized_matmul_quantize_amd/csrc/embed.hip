@@ -165,94 +165,198 @@ hipError_t embed_rows(const E *table, int64_t vocab, int64_t k, const int32_t *i
 // ------------------------------------------------------------------------------------------------
 // Gradient
 // ------------------------------------------------------------------------------------------------
-template <class E>
-__global__ __launch_bounds__(256) void fill_zero_kernel(E *__restrict__ p, int64_t n16, int64_t n) {
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n16; i += (int64_t)gridDim.x * 256)
-        ((u32x4 *)p)[i] = u32x4{0, 0, 0, 0};
-    constexpr int per = 16 / sizeof(E);
-    if (blockIdx.x == 0)
-        for (int64_t i = n16 * per + threadIdx.x; i < n; i += 256) p[i] = (E)0.f;
-}
-
-// Chunks of kChunk sorted tokens; a workgroup sums the rows of one chunk, N columns a thread, from
-// one id to the next.  An id whose tokens lie in one chunk is written at once; the others leave
-// their sums in part[chunk][0] (the id began before this chunk) or part[chunk][1] (it goes on
-// after it), which join_kernel adds up in chunk order: the sum's order is fixed.
+// The gradient is bound by the write of the whole table (most of whose rows no token names), so it is
+// written once: a launch sums the rows that have tokens and clears others beside that, which it tells
+// apart by a search in the sorted ids.
+//
+// Sums: chunks of kChunk sorted tokens; a workgroup sums the rows of one chunk, N columns (16 bytes) a
+// thread, from one id to the next, eight rows in flight.  An id whose tokens lie in one chunk is written
+// at once; the others leave their sums in part[chunk][0] (the id began before this chunk) or
+// part[chunk][1] (it goes on after it), which a second launch adds up in chunk order: the sum's order is
+// fixed.
 constexpr int kChunk = 32;
 
-template <class E, class O, int N>
-__global__ __launch_bounds__(256) void grad_kernel(const E *__restrict__ dy, int64_t k, const int32_t *__restrict__ skeys,
-                                                   const int32_t *__restrict__ order, int64_t n, int32_t vocab,
-                                                   float scale, O *__restrict__ grad, float *__restrict__ part) {
-    const int64_t c = blockIdx.x, e0 = c * kChunk;
-    const int cnt = (int)(n - e0 < kChunk ? n - e0 : kChunk);
-    const int64_t col = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * N;
-    if (col >= k) return;
-    int32_t cur = skeys[e0];
-    bool starts = e0 == 0 || skeys[e0 - 1] != cur;
+struct Grad {
+    const void *dy;
+    const int32_t *skeys, *order;
+    void *grad;
+    float *part;
+    int64_t n, k, vocab;
+    int64_t chunks, slices;     // workgroups of the sums or joins: chunks x slices of the columns
+    int64_t row0, row1;         // table rows to clear where no token names them,
+    int64_t fill_rows;          // this many a workgroup
+    int64_t blocks;
+    float scale;
+};
+
+template <class E, class O, int N> __device__ __forceinline__ void sum_chunk(const Grad &a, int64_t c, int64_t slice) {
+    const E *dy = (const E *)a.dy;
+    const int64_t e0 = c * kChunk;
+    const int cnt = (int)(a.n - e0 < kChunk ? a.n - e0 : kChunk);
+    const int64_t col = (slice * blockDim.x + threadIdx.x) * N;
+    const int32_t vocab = (int32_t)a.vocab;
+    const bool mine = col < a.k;
+    const E *at = dy + (mine ? col : 0);
+    int32_t cur = a.skeys[e0];
+    bool starts = e0 == 0 || a.skeys[e0 - 1] != cur;
     float acc[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) acc[j] = 0.f;
     auto flush = [&](bool ends) {
+        if (!mine) return;
         if (starts && ends) {
 #pragma unroll
-            for (int j = 0; j < N; ++j) acc[j] *= scale;
-            store_n<N>(grad + cur * k + col, acc);
+            for (int j = 0; j < N; ++j) acc[j] *= a.scale;
+            store_n<N>((O *)a.grad + cur * a.k + col, acc);
         } else {
-            store_n<N>(part + (2 * c + (starts ? 1 : 0)) * k + col, acc);
+            store_n<N>(a.part + (2 * c + (starts ? 1 : 0)) * a.k + col, acc);
         }
     };
-    for (int e = 0; e < cnt && cur < vocab; ++e) {
-        const int32_t key = skeys[e0 + e];
-        if (key != cur) {
-            flush(true);
-            cur = key;
-            starts = true;
+    for (int e = 0; e < cnt && cur < vocab; e += 8) {
+        float v[8][N];
 #pragma unroll
-            for (int j = 0; j < N; ++j) acc[j] = 0.f;
-            if (key >= vocab) break;
+        for (int u = 0; u < 8; ++u) load_n<N>(at + a.order[e0 + (e + u < cnt ? e + u : cnt - 1)] * a.k, v[u]);
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+#pragma unroll
+            for (int j = 0; j < N; ++j) asm volatile("" : "+v"(v[u][j]));   // loaded here, not one by one at their use
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (e + u >= cnt || cur >= vocab) break;
+            const int32_t key = a.skeys[e0 + e + u];
+            if (key != cur) {
+                flush(true);
+                cur = key;
+                starts = true;
+#pragma unroll
+                for (int j = 0; j < N; ++j) acc[j] = 0.f;
+                if (key >= vocab) break;
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) acc[j] += v[u][j];
         }
-        float v[N];
-        load_n<N>(dy + order[e0 + e] * k + col, v);
-#pragma unroll
-        for (int j = 0; j < N; ++j) acc[j] += v[j];
     }
-    if (cur < vocab) flush(e0 + cnt == n || skeys[e0 + cnt] != cur);
+    if (cur < vocab) flush(e0 + cnt == a.n || a.skeys[e0 + cnt] != cur);
 }
 
-template <class O, int N>
-__global__ __launch_bounds__(256) void join_kernel(const float *__restrict__ part, int64_t k,
-                                                   const int32_t *__restrict__ skeys, int64_t n, int32_t vocab,
-                                                   float scale, O *__restrict__ grad) {
-    const int64_t c = blockIdx.x, e0 = c * kChunk, e1 = e0 + kChunk;
-    if (e1 >= n) return;
-    const int32_t key = skeys[e1 - 1];
-    // only the chunk in which an id begins that goes on after it
-    if (key >= vocab || skeys[e1] != key || (skeys[e0] == key && e0 > 0 && skeys[e0 - 1] == key)) return;
-    const int64_t col = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * N;
-    if (col >= k) return;
-    float acc[N], v[N];
-    load_n<N>(part + (2 * c + 1) * k + col, acc);
-    for (int64_t q = c + 1; q * kChunk < n && skeys[q * kChunk] == key; ++q) {
-        load_n<N>(part + 2 * q * k + col, v);
-#pragma unroll
-        for (int j = 0; j < N; ++j) acc[j] += v[j];
+// First place of the sorted keys that is >= key, by a whole wave: 64 probes a round.
+__device__ __forceinline__ int64_t lower_bound(const int32_t *skeys, int64_t n, int64_t key) {
+    int64_t lo = 0, hi = n;   // the answer is in [lo, hi]
+    while (lo < hi) {
+        const int64_t step = (hi - lo + 63) / 64, at = lo + (threadIdx.x & 63) * step;
+        const int below = __popcll(__ballot(at < hi && skeys[at < hi ? at : hi - 1] < key));
+        if (below == 0) return lo;
+        lo += (below - 1) * step + 1;
+        if (lo + step - 1 < hi) hi = lo + step - 1;
     }
-#pragma unroll
-    for (int j = 0; j < N; ++j) acc[j] *= scale;
-    store_n<N>(grad + key * k + col, acc);
+    return lo;
 }
 
-template <class E, class O, int N>
-hipError_t grad_n(const E *dy, int64_t n, int64_t k, const int32_t *order, const int32_t *skeys, int64_t vocab,
-                  float scale, O *grad, float *part, hipStream_t s) {
-    const int64_t groups = (k + N - 1) / N;
-    const int threads = groups >= 256 ? 256 : (int)((groups + 63) / 64 * 64);
-    const dim3 grid((unsigned)((n + kChunk - 1) / kChunk), (unsigned)((groups + threads - 1) / threads));
-    hipLaunchKernelGGL((grad_kernel<E, O, N>), grid, dim3(threads), 0, s, dy, k, skeys, order, n, (int32_t)vocab, scale,
-                       grad, part);
-    hipLaunchKernelGGL((join_kernel<O, N>), grid, dim3(threads), 0, s, part, k, skeys, n, (int32_t)vocab, scale, grad);
+constexpr int kMaxFill = 1024;
+
+template <class O, int N> __device__ __forceinline__ void clear_rows(const Grad &a, int64_t v0, uint8_t *named) {
+    const int rows = (int)(a.row1 - v0 < a.fill_rows ? a.row1 - v0 : a.fill_rows);
+    for (int i = threadIdx.x; i < rows; i += blockDim.x) named[i] = 0;
+    __syncthreads();
+    const int64_t lo = lower_bound(a.skeys, a.n, v0), hi = lower_bound(a.skeys, a.n, v0 + rows);
+    for (int64_t i = lo + threadIdx.x; i < hi; i += blockDim.x) named[a.skeys[i] - v0] = 1;
+    __syncthreads();
+    const int groups = (int)(a.k / N);
+    float z[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) z[j] = 0.f;
+    O *g = (O *)a.grad + v0 * a.k;
+    if (groups >= (int)blockDim.x) {
+        for (int r = 0; r < rows; ++r)
+            if (!named[r])
+                for (int i = threadIdx.x; i < groups; i += blockDim.x) store_n<N>(g + r * a.k + (int64_t)i * N, z);
+    } else {
+        for (int i = threadIdx.x; i < rows * groups; i += blockDim.x)
+            if (!named[i / groups]) store_n<N>(g + (int64_t)i * N, z);
+    }
+}
+
+// Only for a chunk in which an id begins that goes on after it.
+template <class O, int N> __device__ __forceinline__ void join_chunk(const Grad &a, int64_t c, int64_t slice) {
+    const int64_t e0 = c * kChunk, e1 = e0 + kChunk;
+    if (e1 >= a.n) return;
+    // every key that decides is loaded before any is looked at
+    auto first_of = [&](int64_t q) { return a.skeys[q * kChunk < a.n ? q * kChunk : e0]; };
+    int32_t key = a.skeys[e1 - 1], after = a.skeys[e1], begin = a.skeys[e0], before = a.skeys[e0 > 0 ? e0 - 1 : 0];
+    int32_t next = first_of(c + 1 + (threadIdx.x & 63));
+    asm volatile("" : "+v"(key), "+v"(after), "+v"(begin), "+v"(before), "+v"(next));
+    key = __builtin_amdgcn_readfirstlane(key);
+    if (key >= a.vocab || after != key || (begin == key && e0 > 0 && before == key)) return;
+    // chunks c + 1 .. last begin with the same id
+    int64_t last = c + 1;
+    for (;;) {
+        const uint64_t other = __ballot((last + (threadIdx.x & 63)) * kChunk >= a.n || next != key);
+        if (other) {
+            last += __ffsll((unsigned long long)other) - 1;
+            break;
+        }
+        last += 64;
+        next = first_of(last + (threadIdx.x & 63));
+    }
+    const int64_t col = (slice * blockDim.x + threadIdx.x) * N;
+    if (col >= a.k) return;
+    float acc[N];
+    load_n<N>(a.part + (2 * c + 1) * a.k + col, acc);
+    for (int64_t q = c + 1; q < last; q += 16) {   // a chunk past the last is read as the last, and left out
+        float v[16][N];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) load_n<N>(a.part + 2 * (q + u < last ? q + u : last - 1) * a.k + col, v[u]);
+#pragma unroll
+        for (int u = 0; u < 16; ++u)
+            for (int j = 0; j < N; ++j) acc[j] += q + u < last ? v[u][j] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) acc[j] *= a.scale;
+    store_n<N>((O *)a.grad + key * a.k + col, acc);
+}
+
+// Sums (or joins) in the first workgroups, clears in the others: N columns a thread of dy or of the
+// partial sums, M of the rows it clears (16 bytes where the rows allow it).
+template <class E, class O, int N, int M, bool JOIN> __global__ __launch_bounds__(256) void grad_kernel(Grad a) {
+    __shared__ uint8_t named[kMaxFill];
+    const int64_t first = a.chunks * a.slices;
+    for (int64_t b = blockIdx.x; b < a.blocks; b += gridDim.x) {
+        if (b < first) {
+            if constexpr (JOIN) join_chunk<O, N>(a, b % a.chunks, b / a.chunks);
+            else sum_chunk<E, O, N>(a, b % a.chunks, b / a.chunks);
+        } else {
+            clear_rows<O, M>(a, a.row0 + (b - first) * a.fill_rows, named);
+            __syncthreads();
+        }
+    }
+}
+
+constexpr int64_t kMaxGrid = 1 << 22;
+int threads_of(int64_t groups) { return groups >= 256 ? 256 : (int)((groups + 63) / 64 * 64); }
+
+template <class E, class O, int N, int M, bool JOIN> hipError_t grad_part(Grad a, int64_t row0, int64_t row1, hipStream_t s) {
+    const int threads = threads_of((a.k + N - 1) / N);
+    a.chunks = (a.n + kChunk - 1) / kChunk;
+    a.slices = a.n ? (a.k + (int64_t)N * threads - 1) / ((int64_t)N * threads) : 0;
+    // about 128 KB a workgroup that clears
+    a.fill_rows = 131072 / (a.k * (int64_t)sizeof(O));
+    a.fill_rows = a.fill_rows < 1 ? 1 : a.fill_rows > kMaxFill ? kMaxFill : a.fill_rows;
+    a.row0 = row0;
+    a.row1 = row1;
+    a.blocks = a.chunks * a.slices + (row1 - row0 + a.fill_rows - 1) / a.fill_rows;
+    hipLaunchKernelGGL((grad_kernel<E, O, N, M, JOIN>), dim3((unsigned)(a.blocks < kMaxGrid ? a.blocks : kMaxGrid)),
+                       dim3(threads), 0, s, a);
     return hipGetLastError();
+}
+
+template <class E, class O, int N, int M> hipError_t grad_n(const Grad &a, hipStream_t s) {
+    // A table beyond the 256 MB cache is cleared half beside the sums and half beside the joins, which
+    // would otherwise wait for its writes to drain (1 GB: 256 against 264 us); a smaller one beside the sums
+    // (131 MB: 39 against 43 us).
+    const int64_t half = a.n > kChunk && a.vocab * a.k * (int64_t)sizeof(O) > (256 << 20) ? a.vocab / 2 : a.vocab;
+    hipError_t e = grad_part<E, O, N, M, false>(a, 0, half, s);
+    if (e != hipSuccess || a.n <= kChunk) return e;
+    return grad_part<float, O, N < 4 ? N : 4, M, true>(a, half, a.vocab, s);
 }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -290,21 +394,28 @@ size_t embed_backward_bytes(int64_t n, int64_t k, int64_t vocab) {
 
 hipError_t launch_embed_backward(int dy_type, const void *dy, int64_t n, int64_t k, const int32_t *ids, int64_t vocab,
                                  float scale, int g_type, void *grad, uint8_t *ws, hipStream_t s) {
-    return with_type(g_type, [&](auto o) -> hipError_t {
-        typedef decltype(o) O;
-        const int64_t cells = vocab * k, n16 = aligned16(grad) ? cells * (int64_t)sizeof(O) / 16 : 0;
-        hipLaunchKernelGGL(fill_zero_kernel<O>, dim3(grid_of(n16)), dim3(256), 0, s, (O *)grad, n16, cells);
-        if (n == 0) return hipGetLastError();
+    Grad a{};
+    a.dy = dy;
+    a.grad = grad;
+    a.n = n;
+    a.k = k;
+    a.vocab = vocab;
+    a.scale = scale;
+    if (n > 0) {
         int32_t *order = (int32_t *)(ws + up256(sort_ids_bytes(n, vocab, true)));
-        float *part = (float *)((uint8_t *)order + up256((size_t)n * 4));
+        a.part = (float *)((uint8_t *)order + up256((size_t)n * 4));
         hipError_t e = launch_sort_ids(ids, n, vocab, order, nullptr, nullptr, true, ws, s);
         if (e != hipSuccess) return e;
-        const int32_t *skeys = sort_ids_keys(ws, n, vocab);
-        return with_type(dy_type, [&](auto i) -> hipError_t {
-            typedef decltype(i) E;
-            if (k % 4 == 0 && aligned16(dy, grad))
-                return grad_n<E, O, 4>((const E *)dy, n, k, order, skeys, vocab, scale, (O *)grad, part, s);
-            return grad_n<E, O, 1>((const E *)dy, n, k, order, skeys, vocab, scale, (O *)grad, part, s);
+        a.skeys = sort_ids_keys(ws, n, vocab);
+        a.order = order;
+    }
+    return with_type(dy_type, [&](auto i) -> hipError_t {
+        typedef decltype(i) E;
+        return with_type(g_type, [&](auto o) -> hipError_t {
+            typedef decltype(o) O;
+            constexpr int N = 16 / sizeof(E), M = 16 / sizeof(O);
+            if (k % (N > M ? N : M) == 0 && aligned16(dy, grad)) return grad_n<E, O, N, M>(a, s);
+            return grad_n<E, O, 1, 1>(a, s);
         });
     });
 }

@@ -73,8 +73,7 @@ __global__ __launch_bounds__(256) void finish_kernel(Finish f) {
 #pragma unroll
                 for (int s = 0; s < 8; ++s) u[s] = *(const f32x4 *)(p + (s0 + s < c.parts ? s0 + s : 0) * next);
 #pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    if (s0 + s < c.parts) sum += u[s];
+                for (int s = 0; s < 8; ++s) sum += s0 + s < c.parts ? u[s] : f32x4{0.f, 0.f, 0.f, 0.f};
             }
             float v[4];
 #pragma unroll

@@ -160,11 +160,11 @@ __global__ __launch_bounds__(256, RT == 8 ? 1 : 2) void narrow_kernel(Args a) {
 
 int tiles_of_rank(int64_t rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
 
-// Slices of K: enough for 256 workgroups, at most 16 partial sums a result, each of 128 values or more.
+// Slices of K: enough for 256 workgroups, at most 8 partial sums a result, each of 128 values or more.
 int slices_of(int64_t n, int64_t k) {
     const int64_t steps = (k + 127) / 128, windows = (n + kWindow - 1) / kWindow;
     int64_t s = 256 / windows;
-    if (s > 16) s = 16;
+    if (s > 8) s = 8;
     if (s > steps) s = steps;
     return s < 1 ? 1 : (int)s;
 }

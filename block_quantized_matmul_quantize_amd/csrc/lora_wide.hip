@@ -95,8 +95,13 @@ __global__ __launch_bounds__(256, KS == 4 ? 1 : 2) void wide_kernel(Args a) {
                         const int j = 256 * u + threadIdx.x, slot = j / (R / 4), r = j % (R / 4) * 4;
                         const float *p = a.part + (i0 + t.row(slot)) * a.padded + (r < a.padded ? r : 0);
                         f32x4 sum = *(const f32x4 *)p;
-#pragma unroll 4
-                        for (int s = 1; s < a.parts; ++s) sum += *(const f32x4 *)(p + s * next);
+                        for (int s0 = 1; s0 < a.parts; s0 += 8) {   // a slice past the last is read as the first, and left out
+                            f32x4 q[8];
+#pragma unroll
+                            for (int s = 0; s < 8; ++s) q[s] = *(const f32x4 *)(p + (s0 + s < a.parts ? s0 + s : 0) * next);
+#pragma unroll
+                            for (int s = 0; s < 8; ++s) sum += s0 + s < a.parts ? q[s] : f32x4{0.f, 0.f, 0.f, 0.f};
+                        }
                         float v[4];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) v[q] = r + q < a.rank ? sum[q] * c : 0.f;   // no other rank is of use
