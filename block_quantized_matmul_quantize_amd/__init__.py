@@ -192,12 +192,12 @@ def matmul_id_glu_workspace(qtype, n_exp, rows, k, n_tok, top_k):
 # Device entry points (torch tensors)
 # --------------------------------------------------------------------------------------------
 def _torch():
-    import torch
     return torch
 
 
 def _stream():
-    return ctypes.c_void_p(_torch().cuda.current_stream().cuda_stream)
+    # torch.cuda.current_stream() without the Stream object it makes, 3 us of a call
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _need(t, dtype, name):
@@ -560,13 +560,24 @@ def _elem(t, name):
     return e
 
 
+def _int32(t, name):
+    """Address of a contiguous int32 tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not torch.int32:
+        raise TypeError(f"{name} must have dtype torch.int32, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
 def _arg(t, dtype, shape, name):
     """Address of a contiguous tensor of this dtype and shape (None: a null pointer)."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
@@ -575,26 +586,26 @@ def _arg(t, dtype, shape, name):
     return t.data_ptr()
 
 
-def _same_device(*tensors):
+def _same_device(first, *others):
     """Last check before pointers cross the C ABI: every tensor lives on the first one's device."""
-    dev = tensors[0].device
-    if dev.type != "cuda":
+    dev = first.get_device()
+    if dev < 0:
         raise ValueError("every tensor must be a device tensor")
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"every tensor must be on {dev}, got {t.device}")
-    return dev
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"every tensor must be on {first.device}, got {t.device}")
 
 
-def _ws_args(ws, nbytes, device):
-    """(address, bytes, tensor to keep until the launch) of a workspace of at least nbytes."""
+def _ws_args(ws, nbytes, like):
+    """(address, bytes, tensor to keep until the launch) of a workspace of at least nbytes on the device
+    of a tensor."""
     if ws is None:
         if nbytes == 0:
             return None, 0, None
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    else:
-        _need(ws, torch.uint8, "ws")
-        _same_device(ws)
+        ws = like.new_empty(nbytes, dtype=torch.uint8)
+        return ws.data_ptr(), nbytes, ws
+    _need(ws, torch.uint8, "ws")
+    _same_device(like, ws)
     return ws.data_ptr(), ws.numel(), ws
 
 
@@ -606,25 +617,25 @@ def sort_ids(ids, n_keys, ws=None):
     """Stable sort of int32 ids (any shape).  Returns int32 (order [n], pos of ids' shape,
     bounds [n_keys + 1]): indices by id with ids outside [0, n_keys) last, each index's place in
     order (-1 for an id outside), and the start of each id's segment."""
-    n = ids.numel() if isinstance(ids, torch.Tensor) else 0
-    pi = _need(ids, torch.int32, "ids")
+    pi = _int32(ids, "ids")
     if n_keys < 1:
         raise ValueError(f"n_keys must be >= 1, got {n_keys}")
-    dev = _same_device(ids)
-    order = torch.empty(n, dtype=torch.int32, device=dev)
-    pos = torch.empty_like(ids)
-    bounds = torch.empty(n_keys + 1, dtype=torch.int32, device=dev)
-    pw, nw, ws = _ws_args(ws, _L.qmm_sort_ids_workspace(n, n_keys), dev)
-    _check(_L.qmm_sort_ids(pi, n, n_keys, order.data_ptr(), pos.data_ptr(), bounds.data_ptr(), pw, nw, _stream()))
+    _same_device(ids)
+    n = ids.numel()
+    order, pos, bounds = ids.new_empty(n), torch.empty_like(ids), ids.new_empty(n_keys + 1)
+    pw, nw, ws = _ws_args(ws, _L.qmm_sort_ids_workspace(n, n_keys), ids)
+    st = _L.qmm_sort_ids(pi, n, n_keys, order.data_ptr(), pos.data_ptr(), bounds.data_ptr(), pw, nw, _stream())
+    if st:
+        _check(st)
     return order, pos, bounds
 
 
 def _valid_count(bounds):
     """Address of the number of valid ids: the last entry of sort_ids' bounds."""
-    _need(bounds, torch.int32, "bounds")
+    p = _int32(bounds, "bounds")
     if bounds.dim() != 1 or bounds.numel() < 2:
         raise ValueError("bounds must be 1-D [n_keys + 1]")
-    return bounds.data_ptr() + 4 * (bounds.numel() - 1)
+    return p + 4 * (bounds.numel() - 1)
 
 
 def _need_pos(pos, name="pos"):
@@ -637,17 +648,20 @@ def gather_sorted(x, pos, bounds, out=None):
     """Rows to expert order: out[pos[t, j]] = x[t] for x [n_tok, k] and sort_ids' pos [n_tok, top_k];
     rows of out [n_tok * top_k, k] past the valid pairs are zeros.  Its gradient: combine(d_out, pos)."""
     e = _elem(x, "x")
-    pp = _need(pos, torch.int32, "pos")
+    pp = _int32(pos, "pos")
     n_tok, top_k = _need_pos(pos)
     if x.dim() != 2 or x.shape[0] != n_tok:
         raise ValueError(f"x must be [{n_tok}, k]")
     k = x.shape[1]
     nv = _valid_count(bounds)
-    if out is None:
-        out = torch.empty((n_tok * top_k, k), dtype=x.dtype, device=x.device)
     po = _arg(out, x.dtype, (n_tok * top_k, k), "out")
     _same_device(x, pos, bounds, out)
-    _check(_L.qmm_gather_sorted(e, x.data_ptr(), n_tok, top_k, k, pp, nv, po, _stream()))
+    if out is None:
+        out = x.new_empty((n_tok * top_k, k))
+        po = out.data_ptr()
+    st = _L.qmm_gather_sorted(e, x.data_ptr(), n_tok, top_k, k, pp, nv, po, _stream())
+    if st:
+        _check(st)
     return out
 
 
@@ -663,18 +677,21 @@ def combine(h, pos=None, weights=None, base=None, out=None):
         n_tok, top_k, k = h.shape
         pp = None
     else:
-        pp = _need(pos, torch.int32, "pos")
+        pp = _int32(pos, "pos")
         n_tok, top_k = _need_pos(pos)
         if h.dim() != 2 or h.shape[0] != n_tok * top_k:
             raise ValueError(f"h must be [{n_tok * top_k}, k]")
         k = h.shape[1]
     pw = _arg(weights, torch.float32, (n_tok, top_k), "weights")
     pb = _arg(base, h.dtype, (n_tok, k), "base")
-    if out is None:
-        out = torch.empty((n_tok, k), dtype=h.dtype, device=h.device)
     po = _arg(out, h.dtype, (n_tok, k), "out")
     _same_device(h, pos, weights, base, out)
-    _check(_L.qmm_combine(e, h.data_ptr(), n_tok, top_k, k, pp, pw, pb, po, _stream()))
+    if out is None:
+        out = h.new_empty((n_tok, k))
+        po = out.data_ptr()
+    st = _L.qmm_combine(e, h.data_ptr(), n_tok, top_k, k, pp, pw, pb, po, _stream())
+    if st:
+        _check(st)
     return out
 
 
@@ -688,7 +705,7 @@ def combine_backward(dy, h, pos=None, weights=None, bounds=None):
         n_tok, top_k, k = h.shape
         pp = nv = None
     else:
-        pp = _need(pos, torch.int32, "pos")
+        pp = _int32(pos, "pos")
         n_tok, top_k = _need_pos(pos)
         if h.dim() != 2 or h.shape[0] != n_tok * top_k:
             raise ValueError(f"h must be [{n_tok * top_k}, k]")
@@ -696,11 +713,12 @@ def combine_backward(dy, h, pos=None, weights=None, bounds=None):
         nv = _valid_count(bounds)
     pd = _arg(dy, h.dtype, (n_tok, k), "dy")
     pw = _arg(weights, torch.float32, (n_tok, top_k), "weights")
-    dev = _same_device(h, dy, pos, weights, bounds)
+    _same_device(h, dy, pos, weights, bounds)
     dh = torch.empty_like(h)
-    dw = torch.empty((n_tok, top_k), dtype=torch.float32, device=dev)
-    _check(_L.qmm_combine_backward(e, pd, h.data_ptr(), n_tok, top_k, k, pp, pw, nv, dh.data_ptr(), dw.data_ptr(),
-                                   _stream()))
+    dw = h.new_empty((n_tok, top_k), dtype=torch.float32)
+    st = _L.qmm_combine_backward(e, pd, h.data_ptr(), n_tok, top_k, k, pp, pw, nv, dh.data_ptr(), dw.data_ptr(), _stream())
+    if st:
+        _check(st)
     return dh, dw
 
 
@@ -708,20 +726,25 @@ def embed(table, qtype, vocab, k, ids, scale=1.0, dtype=torch.float32, out=None)
     """out[i] = scale * table[ids[i]] (zeros for an id outside [0, vocab)).  table: fp32, fp16 or bf16
     [vocab, k] (qtype F32, F16, BF16), or uint8 rows of GGUF blocks; ids int32 of any shape; out
     ids.shape + [k] of dtype.  With ids 0 .. vocab - 1 it expands a block-quantized matrix."""
-    pt = _need(table, _ELEM_DTYPES.get(qtype, torch.uint8), "table")
-    pi = _need(ids, torch.int32, "ids")
-    if qtype in _ELEM_DTYPES:
-        _need_size(table, vocab * k * table.element_size(), "table")
-    else:
+    pi = _int32(ids, "ids")
+    tt = _ELEM_DTYPES.get(qtype)
+    pt = _need(table, torch.uint8 if tt is None else tt, "table")
+    if tt is None:
         _need_weights(table, qtype, vocab, k, "table")
-    if dtype not in _ELEM_TYPES:
+    else:
+        _need_size(table, vocab * k * table.element_size(), "table")
+    e = _ELEM_TYPES.get(dtype)
+    if e is None:
         raise TypeError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
     shape = (*ids.shape, k)
-    if out is None:
-        out = torch.empty(shape, dtype=dtype, device=ids.device)
     po = _arg(out, dtype, shape, "out")
-    _same_device(table, ids, out)
-    _check(_L.qmm_embed(qtype, pt, vocab, k, pi, ids.numel(), scale, _ELEM_TYPES[dtype], po, _stream()))
+    _same_device(ids, table, out)
+    if out is None:
+        out = ids.new_empty(shape, dtype=dtype)
+        po = out.data_ptr()
+    st = _L.qmm_embed(qtype, pt, vocab, k, pi, ids.numel(), scale, e, po, _stream())
+    if st:
+        _check(st)
     return out
 
 
@@ -733,20 +756,24 @@ def embed_backward(dy, ids, vocab, scale=1.0, dtype=torch.float32, out=None, ws=
     """Gradient of embed with respect to a table of elements: [vocab, k] of dtype, every row written;
     dy: ids.shape + [k]."""
     e = _elem(dy, "dy")
-    pi = _need(ids, torch.int32, "ids")
+    pi = _int32(ids, "ids")
     if dy.dim() < 1 or dy.shape[:-1] != ids.shape:
         raise ValueError(f"dy must be {list(ids.shape)} + [k]")
-    if dtype not in _ELEM_TYPES:
+    g = _ELEM_TYPES.get(dtype)
+    if g is None:
         raise TypeError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
     if vocab < 1:
         raise ValueError(f"vocab must be >= 1, got {vocab}")
     n, k = ids.numel(), dy.shape[-1]
-    dev = _same_device(dy, ids, out)
-    if out is None:
-        out = torch.empty((vocab, k), dtype=dtype, device=dev)
     po = _arg(out, dtype, (vocab, k), "out")
-    pw, nw, ws = _ws_args(ws, _L.qmm_embed_backward_workspace(n, k, vocab), dev)
-    _check(_L.qmm_embed_backward(e, dy.data_ptr(), n, k, pi, vocab, scale, _ELEM_TYPES[dtype], po, pw, nw, _stream()))
+    _same_device(dy, ids, out)
+    if out is None:
+        out = dy.new_empty((vocab, k), dtype=dtype)
+        po = out.data_ptr()
+    pw, nw, ws = _ws_args(ws, _L.qmm_embed_backward_workspace(n, k, vocab), dy)
+    st = _L.qmm_embed_backward(e, dy.data_ptr(), n, k, pi, vocab, scale, g, po, pw, nw, _stream())
+    if st:
+        _check(st)
     return out
 
 
@@ -774,14 +801,17 @@ def lora(x, a, b, ids, scale=None, base=None, out=None, keep_h=False, ws=None):
     [n_adapters]; out may be base.  keep_h: returns (out, fp32 a[c] @ x[i] [n, rank]) for the backward."""
     e, w, n, k, na, rank, rows, ps = _lora_shapes(x, a, b, ids, scale)
     pb = _arg(base, x.dtype, (n, rows), "base")
-    dev = _same_device(x, a, b, ids, scale, base, out)
-    if out is None:
-        out = torch.empty((n, rows), dtype=x.dtype, device=dev)
     po = _arg(out, x.dtype, (n, rows), "out")
-    h = torch.empty((n, rank), dtype=torch.float32, device=dev) if keep_h else None
-    pw, nw, ws = _ws_args(ws, _L.qmm_lora_workspace(n, k, rows, rank, na), dev)
-    _check(_L.qmm_lora(e, w, x.data_ptr(), n, k, a.data_ptr(), b.data_ptr(), rows, rank, na, ids.data_ptr(), ps, pb,
-                       po, h.data_ptr() if keep_h else None, pw, nw, _stream()))
+    _same_device(x, a, b, ids, scale, base, out)
+    if out is None:
+        out = x.new_empty((n, rows))
+        po = out.data_ptr()
+    h = x.new_empty((n, rank), dtype=torch.float32) if keep_h else None
+    pw, nw, ws = _ws_args(ws, _L.qmm_lora_workspace(n, k, rows, rank, na), x)
+    st = _L.qmm_lora(e, w, x.data_ptr(), n, k, a.data_ptr(), b.data_ptr(), rows, rank, na, ids.data_ptr(), ps, pb, po,
+                     h.data_ptr() if keep_h else None, pw, nw, _stream())
+    if st:
+        _check(st)
     return (out, h) if keep_h else out
 
 
@@ -797,13 +827,14 @@ def lora_backward(x, dy, h, a, b, ids, scale=None, dx_base=None, need_dx=True, n
     pd = _arg(dy, x.dtype, (n, rows), "dy")
     ph = _arg(h, torch.float32, (n, rank), "h")
     px = _arg(dx_base, x.dtype, (n, k), "dx_base")
-    dev = _same_device(x, a, b, ids, scale, dy, h, dx_base)
+    _same_device(x, a, b, ids, scale, dy, h, dx_base)
     dx = torch.empty_like(x) if need_dx else None
-    da = torch.empty((na, rank, k), dtype=torch.float32, device=dev) if need_dw else None
-    db = torch.empty((na, rows, rank), dtype=torch.float32, device=dev) if need_dw else None
-    pw, nw, ws = _ws_args(ws, _L.qmm_lora_backward_workspace(n, k, rows, rank, na), dev)
-    _check(_L.qmm_lora_backward(e, w, x.data_ptr(), pd, ph, n, k, a.data_ptr(), b.data_ptr(), rows, rank, na,
-                                ids.data_ptr(), ps, px, dx.data_ptr() if need_dx else None,
-                                da.data_ptr() if need_dw else None, db.data_ptr() if need_dw else None, pw, nw,
-                                _stream()))
+    da = a.new_empty(a.shape, dtype=torch.float32) if need_dw else None
+    db = b.new_empty(b.shape, dtype=torch.float32) if need_dw else None
+    pw, nw, ws = _ws_args(ws, _L.qmm_lora_backward_workspace(n, k, rows, rank, na), x)
+    st = _L.qmm_lora_backward(e, w, x.data_ptr(), pd, ph, n, k, a.data_ptr(), b.data_ptr(), rows, rank, na, ids.data_ptr(),
+                              ps, px, dx.data_ptr() if need_dx else None, da.data_ptr() if need_dw else None,
+                              db.data_ptr() if need_dw else None, pw, nw, _stream())
+    if st:
+        _check(st)
     return dx, da, db
