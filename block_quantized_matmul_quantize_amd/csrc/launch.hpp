@@ -186,9 +186,12 @@ struct LoraCall {
 // Padded rank of the partial and dh rows; slices of K that a product of k values a row is split into.
 int lora_padded_rank(int64_t rank);
 int lora_narrow_slices(int64_t n, int64_t k);
+// Whether the launch below can also sort the rows (order not null) for this many rows and adapters.
+bool lora_narrow_sorts(int64_t n, int64_t n_adapters);
 // part [slices][n][padded rank] = v [n][k] times the row's matrix: m [rank][k] (by_row) or [k][rank] of each adapter.
 hipError_t launch_lora_narrow(int x_type, int w_type, bool by_row, const void *v, int64_t n, int64_t k, const void *m,
-                              int64_t rank, int64_t n_adapters, const int32_t *ids, float *part, hipStream_t s);
+                              int64_t rank, int64_t n_adapters, const int32_t *ids, float *part, int32_t *order,
+                              int32_t *pos, int32_t *bounds, hipStream_t s);
 // Between the two halves: sums of the slices, and what the gradients of A and B need.
 struct LoraFinish {
     const float *part;      // or null: only kept

@@ -137,7 +137,8 @@ size_t lora_backward_bytes(int64_t n, int64_t k, int64_t rows, int64_t rank, int
 
 hipError_t launch_lora(const LoraCall &c, const void *base, void *y, float *h_out, uint8_t *ws, hipStream_t s) {
     float *part = (float *)ws;
-    hipError_t e = launch_lora_narrow(c.x_type, c.w_type, true, c.x, c.n, c.k, c.a, c.rank, c.n_adapters, c.ids, part, s);
+    hipError_t e = launch_lora_narrow(c.x_type, c.w_type, true, c.x, c.n, c.k, c.a, c.rank, c.n_adapters, c.ids, part,
+                                      nullptr, nullptr, nullptr, s);
     if (e != hipSuccess) return e;
     int parts = lora_narrow_slices(c.n, c.k);
     if (h_out || (c.n > kSumRows && parts > 1)) {
@@ -165,13 +166,16 @@ hipError_t launch_lora_backward(const LoraCall &c, const void *dy, const float *
     uint16_t *parts_h = (uint16_t *)(ws + L.parts_h), *parts_dh = (uint16_t *)(ws + L.parts_dh);
     float *part = (float *)(ws + L.part);
     hipError_t e = hipSuccess;
-    if (da || db) {
+    // where the first product runs anyway, one of its workgroups sorts the rows
+    const bool beside = (da || db) && c.n > 0 && (dx || da) && lora_narrow_sorts(c.n, c.n_adapters);
+    if ((da || db) && !beside) {
         e = launch_sort_ids(c.ids, c.n, c.n_adapters, order, pos, bounds, false, ws, s);
         if (e != hipSuccess) return e;
     }
     if (c.n > 0) {
         if (dx || da) {
-            e = launch_lora_narrow(c.x_type, c.w_type, false, dy, c.n, c.rows, c.b, c.rank, c.n_adapters, c.ids, part, s);
+            e = launch_lora_narrow(c.x_type, c.w_type, false, dy, c.n, c.rows, c.b, c.rank, c.n_adapters, c.ids, part,
+                                   beside ? order : nullptr, pos, bounds, s);
             if (e != hipSuccess) return e;
         }
         int parts = lora_narrow_slices(c.n, c.rows);

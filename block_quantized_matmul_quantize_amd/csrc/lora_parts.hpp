@@ -49,13 +49,15 @@ __device__ __forceinline__ Tiles find_tiles(const int32_t *__restrict__ ids, int
 struct Tile {
     int32_t key;    // adapter
     int rows;       // 1 .. 64
-    int at;         // lane l < rows: row of slot l within the window
-    __device__ __forceinline__ int row(int slot) const { return __shfl(at, slot < rows ? slot : 0); }
+    int slot0;      // first slot
+    int at;         // lane l: row of slot l within the window
+    __device__ __forceinline__ int row(int slot) const { return __shfl(at, slot0 + (slot < rows ? slot : 0)); }
 };
 __device__ __forceinline__ Tile pick_tile(const Tiles &t, int i) {
     const uint64_t m = __ballot(t.tile == i);
     Tile r;
     r.rows = __popcll(m);
+    r.slot0 = 0;
     r.key = __builtin_amdgcn_readlane(t.key, lowest(m));
     // each row's lane number goes to the lane of its slot; the other lanes push to lane 63, which is a
     // slot only where there are no other lanes
@@ -63,6 +65,13 @@ __device__ __forceinline__ Tile pick_tile(const Tiles &t, int i) {
     return r;
 }
 
+// One of four parts of a tile, 16 slots each (without rows where the tile has fewer).
+__device__ __forceinline__ Tile part_of(const Tile &t, int part) {
+    Tile r = t;
+    r.slot0 = 16 * part;
+    r.rows = t.rows - r.slot0 < 16 ? t.rows - r.slot0 : 16;
+    return r;
+}
 // Calls f(number of 16-row groups, 1, 2 or 4): a wave takes all of them, so that its operand of the
 // adapter's matrix, once loaded, serves every row of the tile.
 template <class F> __device__ __forceinline__ void with_groups(const Tile &t, F f) {
@@ -82,12 +91,18 @@ inline int64_t tiles_of_window(int64_t n, int64_t n_adapters) {
     return n < most ? n : most;
 }
 // Workgroups that share a window's tiles: one for each tile there can be as long as the launch stays
-// at about 4096 workgroups, else 2 (runs of rows of one request give a window one or two tiles);
-// those that find no tile end after reading the ids.
+// at about 1024 workgroups, else 2 (runs of rows of one request give a window one or two tiles); those
+// that find no tile end after reading the ids, but hold a place on a compute unit until then.
 inline int tile_lanes(int64_t others, int64_t n, int64_t n_adapters) {
-    const int64_t most = tiles_of_window(n, n_adapters), fit = 4096 / others;
+    const int64_t most = tiles_of_window(n, n_adapters), fit = 1024 / others;
     const int64_t least = most < 2 ? most : 2;
     return (int)(fit > most ? most : fit < least ? least : fit);
+}
+// Workgroups that a tile's rows are spread over: a small call, which latency bounds, has each take 16 rows,
+// if adapters have that many (300 rows of 2 adapters into 2048 columns: 8.7 against 13.7 us; 32 rows of 64
+// adapters: 14.2 against 7.0 us).
+inline int tile_parts(int64_t others, int lanes, int64_t n, int64_t n_adapters) {
+    return others * lanes * 4 <= 1024 && n_adapters * 16 <= n ? 4 : 1;
 }
 // Slices of the other dimension x windows (the kernels step through what exceeds the grid) x workgroups
 // of a window, which come last: workgroups go round the compute units in order, so that those without a
@@ -99,7 +114,7 @@ inline dim3 tile_grid(int64_t slices, int lanes, int64_t n) {
 // The slice of a workgroup: turned by one from window to window.  Workgroups go round the eight dies, so
 // with 8 slices each die would otherwise see one range of columns only, and rows a multiple of 4 KB
 // apart would share few of its L2 channels.
-__device__ __forceinline__ int64_t slice_of_block() { return (blockIdx.x + blockIdx.y) % gridDim.x; }
+__device__ __forceinline__ int64_t slice_of_block(int64_t slices) { return (blockIdx.x + blockIdx.y) % slices; }
 // Host: calls f(values of the element types of x and of the adapters).
 template <class F> hipError_t with_lora_types(int x_type, int w_type, F f) {
     return with_type(x_type, [&](auto x) -> hipError_t {

@@ -25,7 +25,7 @@ struct Args {
     const int32_t *ids;
     const float *scale;
     int64_t n, cols, slice;
-    int32_t n_adapters, key_bits, rank, padded, parts, slices, lanes;
+    int32_t n_adapters, key_bits, rank, padded, parts, slices, lanes, row_parts;
 };
 
 template <int R> struct Stage {
@@ -57,12 +57,14 @@ __global__ __launch_bounds__(256, KS == 4 ? 1 : 2) void wide_kernel(Args a) {
     constexpr int V = kPiece;
     __shared__ alignas(16) Stage<R> stage;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, m = lane & 15, g = lane >> 4;
-    const int64_t slice = slice_of_block();
+    const int64_t slice = slice_of_block(a.slices);
     const int64_t lo = slice * a.slice, hi = lo + a.slice < a.cols ? lo + a.slice : a.cols;
     for (int64_t i0 = (int64_t)blockIdx.y * kWindow; i0 < a.n; i0 += (int64_t)gridDim.y * kWindow) {
         const Tiles tiles = find_tiles(a.ids, i0, a.n, a.n_adapters, a.key_bits, true);
-        for (int i = blockIdx.z; i < tiles.count; i += gridDim.z) {
-            const Tile t = pick_tile(tiles, i);
+        for (int i = blockIdx.z % a.lanes; i < tiles.count; i += a.lanes) {
+            Tile t = pick_tile(tiles, i);
+            if (a.row_parts > 1) t = part_of(t, blockIdx.z / a.lanes);
+            if (t.rows <= 0) continue;
             const bool some = t.key < a.n_adapters;
             with_groups(t, [&](auto groups) {
                 constexpr int MT = decltype(groups)::value;
@@ -87,6 +89,38 @@ __global__ __launch_bounds__(256, KS == 4 ? 1 : 2) void wide_kernel(Args a) {
                 };
                 int64_t c0 = lo + wave * (16 * V);
                 if (base && c0 < hi) load_base(c0);
+                // the adapter's part for 32 ranks from 32 * s and the columns of a step
+                auto load_w = [&](int64_t at, int s, Raw8<W> (&raw)[V]) {
+                    const int64_t col = col_of(at);
+                    const int nw = width_of(col), r0 = 32 * s + 8 * g;
+                    if constexpr (KM) {
+#pragma unroll
+                        for (int q = 0; q < V; ++q) {
+                            const W *p = w + (col + (OV || q < nw ? q : nw - 1)) * a.rank;
+                            if constexpr (WV) raw[q] = load8(p + (r0 < a.rank ? r0 : 0));
+                            else raw[q] = load8<false>(p + r0, a.rank - r0);
+                        }
+                        if (WV && a.rank < R && r0 >= a.rank)
+#pragma unroll
+                            for (int q = 0; q < V; ++q) raw[q] = Raw8<W>{};
+                    } else {
+                        Rows8<W, V> rows;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            rows.row[e] = load_row<OV, V>(w + (r0 + e < a.rank ? r0 + e : 0) * a.cols + col, nw);
+                        if (a.rank < R)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (r0 + e >= a.rank)
+#pragma unroll
+                                    for (int q = 0; q < V; ++q) rows.row[e].v[q] = (W)0.f;
+#pragma unroll
+                        for (int q = 0; q < V; ++q) raw[q] = rows.column(q);
+                    }
+                };
+                // up to 32 ranks of the first step before h is there, so that one latency covers both
+                Raw8<W> raw[V];
+                if (KS == 1 && some && c0 < hi) load_w(c0, 0, raw);
                 if (some) {
                     const float c = a.scale ? a.scale[t.key] : 1.f;
                     const int64_t next = a.n * a.padded;
@@ -121,31 +155,7 @@ __global__ __launch_bounds__(256, KS == 4 ? 1 : 2) void wide_kernel(Args a) {
 #pragma unroll
                         for (int s = 0; s < KS; ++s) {
                             const int r0 = 32 * s + 8 * g;
-                            Raw8<W> raw[V];
-                            if constexpr (KM) {
-#pragma unroll
-                                for (int q = 0; q < V; ++q) {
-                                    const W *p = w + (col + (OV || q < nw ? q : nw - 1)) * a.rank;
-                                    if constexpr (WV) raw[q] = load8(p + (r0 < a.rank ? r0 : 0));
-                                    else raw[q] = load8<false>(p + r0, a.rank - r0);
-                                }
-                                if (WV && a.rank < R && r0 >= a.rank)
-#pragma unroll
-                                    for (int q = 0; q < V; ++q) raw[q] = Raw8<W>{};
-                            } else {
-                                Rows8<W, V> rows;
-#pragma unroll
-                                for (int e = 0; e < 8; ++e)
-                                    rows.row[e] = load_row<OV, V>(w + (r0 + e < a.rank ? r0 + e : 0) * a.cols + col, nw);
-                                if (a.rank < R)
-#pragma unroll
-                                    for (int e = 0; e < 8; ++e)
-                                        if (r0 + e >= a.rank)
-#pragma unroll
-                                            for (int q = 0; q < V; ++q) rows.row[e].v[q] = (W)0.f;
-#pragma unroll
-                                for (int q = 0; q < V; ++q) raw[q] = rows.column(q);
-                            }
+                            if constexpr (KS > 1) load_w(c0, s, raw);
                             decltype(parts_of<false>(raw[0])) f[V];
 #pragma unroll
                             for (int q = 0; q < V; ++q) f[q] = parts_of<false>(raw[q]);
@@ -167,6 +177,7 @@ __global__ __launch_bounds__(256, KS == 4 ? 1 : 2) void wide_kernel(Args a) {
                     const bool in = c0 + V * m < hi;
                     const int64_t at = c0 + 64 * V;
                     if (base && at < hi) load_base(at);
+                    if (KS == 1 && some && at < hi) load_w(at, 0, raw);
 #pragma unroll
                     for (int u = 0; u < MT; ++u)
 #pragma unroll
@@ -192,7 +203,7 @@ __global__ __launch_bounds__(256, KS == 4 ? 1 : 2) void wide_kernel(Args a) {
 }
 
 template <class X, class W, bool KM> hipError_t launch(const Args &a, bool ov, bool wv, hipStream_t st) {
-    const dim3 grid = tile_grid(a.slices, a.lanes, a.n);
+    const dim3 grid = tile_grid(a.slices, a.lanes * a.row_parts, a.n);
     auto go = [&](auto ks) -> hipError_t {
         constexpr int KS = decltype(ks)::value;
         if (ov && wv)
@@ -233,6 +244,7 @@ hipError_t launch_lora_wide(int x_type, int w_type, bool by_row, const float *pa
     while (a.slice < 256 * kPiece && windows * ((cols + 2 * a.slice - 1) / (2 * a.slice)) >= 512) a.slice *= 2;
     a.slices = (int32_t)((cols + a.slice - 1) / a.slice);
     a.lanes = tile_lanes(windows * a.slices, n, n_adapters);
+    a.row_parts = tile_parts(windows * a.slices, a.lanes, n, n_adapters);
     return with_lora_types(x_type, w_type, [&](auto x, auto w) -> hipError_t {
         typedef decltype(x) X;
         typedef decltype(w) W;
