@@ -5,7 +5,7 @@
 // It reads base and writes out, 8 bytes an fp32 result, against a few operations for each: HBM bounds
 // it.  A workgroup takes the rows of one adapter in a window of 64 and a slice of the columns; it adds
 // up the slices of its rows' h and leaves their bf16 parts in LDS.  A wave takes 64 columns at a time for
-// all the rows: it loads the adapter's part for them once, and holds base for 64 rows (16 KB) in flight.
+// all the rows, 32 of them together: it loads the adapter's part for them once.
 // Lane l % 16 owns four neighbouring columns of a row, so that base is read and out written 256 (fp32)
 // or 128 bytes a row at a time, straight from the accumulators: column q of the lanes' pieces is one
 // matrix instruction's 16 columns.
@@ -67,12 +67,12 @@ __global__ __launch_bounds__(256, KS == 4 ? 1 : 2) void wide_kernel(Args a) {
             if (t.rows <= 0) continue;
             const bool some = t.key < a.n_adapters;
             with_groups(t, [&](auto groups) {
-                constexpr int MT = decltype(groups)::value;
+                constexpr int G = decltype(groups)::value, MT = G < 2 ? 1 : 2;   // groups of 16 rows, and at a time
                 const X *base = (const X *)a.base;
                 const W *w = (const W *)a.m + (int64_t)t.key * a.rank * a.cols;
-                int32_t row[MT][4];
+                int32_t row[G][4];
 #pragma unroll
-                for (int u = 0; u < MT; ++u)
+                for (int u = 0; u < G; ++u)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)   // slots past the last: row of slot 0, not stored
                         row[u][e] = (int32_t)i0 + t.row(16 * u + 4 * g + e);
@@ -80,15 +80,15 @@ __global__ __launch_bounds__(256, KS == 4 ? 1 : 2) void wide_kernel(Args a) {
                 auto col_of = [&](int64_t at) { return at + V * m < hi ? at + V * m : OV ? hi - V : hi - 1; };
                 auto width_of = [&](int64_t col) { return OV || hi - col >= V ? V : (int)(hi - col); };
                 Piece<X, V> b[MT][4];
-                auto load_base = [&](int64_t at) {
+                auto load_base = [&](int64_t at, int u0) {
                     const int64_t col = col_of(at);
 #pragma unroll
                     for (int u = 0; u < MT; ++u)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) b[u][e] = load_row<OV, V>(base + row[u][e] * a.cols + col, width_of(col));
+                        for (int e = 0; e < 4; ++e) b[u][e] = load_row<OV, V>(base + row[u0 + u][e] * a.cols + col, width_of(col));
                 };
                 int64_t c0 = lo + wave * (16 * V);
-                if (base && c0 < hi) load_base(c0);
+                if (base && c0 < hi) load_base(c0, 0);
                 // the adapter's part for 32 ranks from 32 * s and the columns of a step
                 auto load_w = [&](int64_t at, int s, Raw8<W> (&raw)[V]) {
                     const int64_t col = col_of(at);
@@ -125,7 +125,7 @@ __global__ __launch_bounds__(256, KS == 4 ? 1 : 2) void wide_kernel(Args a) {
                     const float c = a.scale ? a.scale[t.key] : 1.f;
                     const int64_t next = a.n * a.padded;
 #pragma unroll
-                    for (int u = 0; u < MT * KS / 2 || u == 0; ++u) {
+                    for (int u = 0; u < G * KS / 2 || u == 0; ++u) {
                         const int j = 256 * u + threadIdx.x, slot = j / (R / 4), r = j % (R / 4) * 4;
                         const float *p = a.part + (i0 + t.row(slot)) * a.padded + (r < a.padded ? r : 0);
                         f32x4 sum = *(const f32x4 *)p;
@@ -144,57 +144,62 @@ __global__ __launch_bounds__(256, KS == 4 ? 1 : 2) void wide_kernel(Args a) {
                     __syncthreads();
                 }
                 for (; c0 < hi; c0 += 64 * V) {
-                    const int64_t col = col_of(c0);
+                    const int64_t col = col_of(c0), at = c0 + 64 * V;
                     const int nw = width_of(col);
-                    f32x4 acc[MT][V];
-#pragma unroll
-                    for (int u = 0; u < MT; ++u)
-#pragma unroll
-                        for (int q = 0; q < V; ++q) acc[u][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    const bool in = c0 + V * m < hi;
+                    decltype(parts_of<false>(raw[0])) f[KS][V];
                     if (some) {
 #pragma unroll
                         for (int s = 0; s < KS; ++s) {
-                            const int r0 = 32 * s + 8 * g;
                             if constexpr (KS > 1) load_w(c0, s, raw);
-                            decltype(parts_of<false>(raw[0])) f[V];
 #pragma unroll
-                            for (int q = 0; q < V; ++q) f[q] = parts_of<false>(raw[q]);
-#pragma unroll
-                            for (int u = 0; u < MT; ++u) {
-                                const Frag<3> h = stage.get(16 * u + m, r0);
-#pragma unroll
-                                for (int q = 0; q < V; ++q) acc[u][q] = mul_acc<bf16_t>(h, f[q], acc[u][q]);
-                            }
+                            for (int q = 0; q < V; ++q) f[s][q] = parts_of<false>(raw[q]);
                         }
+                        if (KS == 1 && at < hi) load_w(at, 0, raw);
                     }
-                    if (base)
+#pragma unroll
+                    for (int u0 = 0; u0 < G; u0 += MT) {
+                        f32x4 acc[MT][V];
 #pragma unroll
                         for (int u = 0; u < MT; ++u)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
+                            for (int q = 0; q < V; ++q) acc[u][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+                        if (some)
 #pragma unroll
-                                for (int q = 0; q < V; ++q) acc[u][q][e] = (float)b[u][e].v[q] + acc[u][q][e];
-                    const bool in = c0 + V * m < hi;
-                    const int64_t at = c0 + 64 * V;
-                    if (base && at < hi) load_base(at);
-                    if (KS == 1 && some && at < hi) load_w(at, 0, raw);
+                            for (int s = 0; s < KS; ++s)
 #pragma unroll
-                    for (int u = 0; u < MT; ++u)
+                                for (int u = 0; u < MT; ++u) {
+                                    const Frag<3> h = stage.get(16 * (u0 + u) + m, 32 * s + 8 * g);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if (16 * u + 4 * g + e >= t.rows || !in) continue;
-                            Piece<X, V> o;
+                                    for (int q = 0; q < V; ++q) acc[u][q] = mul_acc<bf16_t>(h, f[s][q], acc[u][q]);
+                                }
+                        if (base)
 #pragma unroll
-                            for (int q = 0; q < V; ++q) o.v[q] = (X)acc[u][q][e];
-                            X *p = (X *)a.out + row[u][e] * a.cols + col;
-                            if constexpr (OV) {
-                                *(Piece<X, V> *)p = o;
-                            } else {
+                            for (int u = 0; u < MT; ++u)
 #pragma unroll
-                                for (int q = 0; q < V; ++q)
-                                    if (q < nw) p[q] = o.v[q];
+                                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                                    for (int q = 0; q < V; ++q) acc[u][q][e] = (float)b[u][e].v[q] + acc[u][q][e];
+                        if (base && u0 + MT < G) load_base(c0, u0 + MT);
+                        else if (base && at < hi) load_base(at, 0);
+#pragma unroll
+                        for (int u = 0; u < MT; ++u)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                if (16 * (u0 + u) + 4 * g + e >= t.rows || !in) continue;
+                                Piece<X, V> o;
+#pragma unroll
+                                for (int q = 0; q < V; ++q) o.v[q] = (X)acc[u][q][e];
+                                X *p = (X *)a.out + row[u0 + u][e] * a.cols + col;
+                                if constexpr (OV) {
+                                    *(Piece<X, V> *)p = o;
+                                } else {
+#pragma unroll
+                                    for (int q = 0; q < V; ++q)
+                                        if (q < nw) p[q] = o.v[q];
+                                }
                             }
-                        }
+                    }
                 }
                 if (some) __syncthreads();
             });
