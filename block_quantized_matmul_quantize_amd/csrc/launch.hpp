@@ -201,8 +201,8 @@ struct LoraFinish {
     const float *scale;
     float *sum;             // or null: [n][padded rank] (may be part: its first slice)
     float *h;               // or null: [n][rank], zeros for a row without an adapter
-    // where not null, the bf16 parts [3][padded rank][lora_parts_stride(n)] of kept [n][rank] and of the scaled sum,
-    // rows at their places pos of the order sorted by adapter
+    // where not null, the bf16 parts [place / 32][3][padded rank][place % 32] of kept [n][rank] and of the scaled
+    // sum, rows at their places pos of the order sorted by adapter
     const float *kept;
     uint16_t *parts_h, *parts_dh;
     const int32_t *pos;
@@ -212,8 +212,6 @@ hipError_t launch_lora_finish(const LoraFinish &c, hipStream_t s);
 hipError_t launch_lora_wide(int x_type, int w_type, bool by_row, const float *part, int parts, int64_t n, int64_t cols,
                             const void *m, int64_t rank, int64_t n_adapters, const int32_t *ids, const float *scale,
                             const void *base, void *out, hipStream_t s);
-// Row stride of the parts.
-int64_t lora_parts_stride(int64_t n);
 size_t lora_outer_bytes(int64_t n, int64_t k, int64_t rows, int64_t rank, int64_t n_adapters);
 // da [n_adapters][rank][k] from x and dh's parts, db [n_adapters][rows][rank] from dy and h's (either may be null).
 hipError_t launch_lora_outer(int x_type, const void *x, const uint16_t *parts_dh, int64_t k, float *da, const void *dy,

@@ -18,7 +18,6 @@ constexpr int64_t kSumRows = 256;
 struct Finish {
     LoraFinish c;
     int32_t padded;
-    int64_t stride;
 };
 
 // A workgroup takes 64 rows and 16 ranks, a thread 4 ranks of a row.
@@ -52,7 +51,7 @@ __global__ __launch_bounds__(256) void finish_kernel(Finish f) {
                 for (int j = 0; j < 3; ++j)
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        out[(j * f.padded + 16 * (int64_t)blockIdx.x + 4 * wave + q) * f.stride + place] =
+                        out[((place / 32 * 3 + j) * f.padded + 16 * blockIdx.x + 4 * wave + q) * 32 + place % 32] =
                             stage[j][lane][4 * wave + q];
             __syncthreads();
         };
@@ -109,9 +108,9 @@ Layout layout(int64_t n, int64_t k, int64_t rows, int64_t rank, int64_t n_adapte
     L.part = off;
     off += n ? up256((size_t)(lora_narrow_slices(n, rows) * n * padded) * 4) : 0;
     L.parts_h = off;
-    off += up256((size_t)(3 * padded * lora_parts_stride(n)) * 2);
+    off += up256((size_t)(3 * padded * ((n + 31) / 32 * 32)) * 2);
     L.parts_dh = off;
-    off += up256((size_t)(3 * padded * lora_parts_stride(n)) * 2);
+    off += up256((size_t)(3 * padded * ((n + 31) / 32 * 32)) * 2);
     L.outer = off;
     off += up256(lora_outer_bytes(n, k, rows, rank, n_adapters));
     L.total = off;
@@ -121,7 +120,7 @@ Layout layout(int64_t n, int64_t k, int64_t rows, int64_t rank, int64_t n_adapte
 }  // namespace
 
 hipError_t launch_lora_finish(const LoraFinish &c, hipStream_t s) {
-    const Finish f{c, lora_padded_rank(c.rank), lora_parts_stride(c.n)};
+    const Finish f{c, lora_padded_rank(c.rank)};
     const int64_t windows = (c.n + kWindow - 1) / kWindow;
     hipLaunchKernelGGL(finish_kernel, dim3((unsigned)(f.padded / 16), (unsigned)(windows < 65535 ? windows : 65535)),
                        dim3(256), 0, s, f);

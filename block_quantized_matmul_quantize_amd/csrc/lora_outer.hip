@@ -4,8 +4,8 @@
 // A workgroup takes 64 or 128 columns of x (or dy) for all ranks of one adapter; its four waves take
 // turns at 32 places of the rows sorted by adapter.  x and dy are read once; K of the products is the
 // row, so every lane reads 8 rows of 4 or 8 neighbouring columns and is itself the transpose that the
-// operand needs, without LDS.  h and dh come as bf16 parts [3][rank][place], operands as they are, from
-// L2, once for each block of columns.  The waves add their sums up in LDS in a fixed order.  An adapter
+// operand needs, without LDS.  h and dh come as bf16 parts [place / 32][3][rank][place % 32], operands
+// as they are and one stretch of memory a step, from L2, once for each block of columns.  The waves add their sums up in LDS in a fixed order.  An adapter
 // with many rows and few columns is split over several workgroups, whose sums a second launch adds up.
 #include "launch.hpp"
 #include "lora_parts.hpp"
@@ -16,7 +16,7 @@ namespace {
 
 struct Job {
     const void *v;
-    const uint16_t *h;      // bf16 parts [3][padded rank][stride]
+    const uint16_t *h;      // bf16 parts [place / 32][3][padded rank][place % 32]
     float *out;
     const float *scale;     // or null
     int64_t cols, slices;
@@ -26,7 +26,7 @@ struct Args {
     Job job[2];
     const int32_t *order, *bounds;
     float *part;            // [splits][n_adapters * rank * (all columns)], where splits > 1
-    int64_t items, out_total, stride;
+    int64_t items, out_total;
     int32_t rank, splits, n_adapters;
 };
 
@@ -79,7 +79,7 @@ __global__ __launch_bounds__(256) void outer_kernel(Args a) {
             for (int p = 0; p < RT; ++p)
 #pragma unroll
                 for (int j = 0; j < 3; ++j)
-                    hf[p].p[j] = *(const u32x4 *)(job.h + (j * R + 16 * p + m) * a.stride + p0 + 8 * g);
+                    hf[p].p[j] = *(const u32x4 *)(job.h + 3 * R * p0 + (j * R + 16 * p + m) * 32 + 8 * g);
             if (p0 < lo || p0 + 32 > hi) {   // places of other adapters
                 u32x4 keep;
 #pragma unroll
@@ -166,8 +166,6 @@ int64_t blocks_of(int x_type, int64_t rank, int64_t cols) {
 
 }  // namespace
 
-int64_t lora_parts_stride(int64_t n) { return (n + 31) / 32 * 32; }
-
 size_t lora_outer_bytes(int64_t n, int64_t k, int64_t rows, int64_t rank, int64_t n_adapters) {
     // for any element type, and either gradient alone: no workgroup count is below the widest blocks'
     size_t most = 0;
@@ -191,7 +189,6 @@ hipError_t launch_lora_outer(int x_type, const void *x, const uint16_t *parts_dh
     a.order = order;
     a.bounds = bounds;
     a.part = part;
-    a.stride = lora_parts_stride(n);
     a.rank = (int32_t)rank;
     a.n_adapters = (int32_t)n_adapters;
     const int rt = rank_tiles(rank);

@@ -5,7 +5,7 @@
 // It reads base and writes out, 8 bytes an fp32 result, against a few operations for each: HBM bounds
 // it.  A workgroup takes the rows of one adapter in a window of 64 and a slice of the columns; it adds
 // up the slices of its rows' h and leaves their bf16 parts in LDS.  A wave takes 64 columns at a time for
-// all the rows, 32 of them together: it loads the adapter's part for them once.
+// all the rows, 16 or 32 of them together: it loads the adapter's part for them once.
 // Lane l % 16 owns four neighbouring columns of a row, so that base is read and out written 256 (fp32)
 // or 128 bytes a row at a time, straight from the accumulators: column q of the lanes' pieces is one
 // matrix instruction's 16 columns.
@@ -52,7 +52,7 @@ template <int R> struct Stage {
 };
 
 template <class X, class W, int KS, bool KM, bool OV, bool WV>
-__global__ __launch_bounds__(256, KS == 4 ? 1 : 2) void wide_kernel(Args a) {
+__global__ __launch_bounds__(256, KS == 4 && sizeof(W) == 4 ? 1 : 2) void wide_kernel(Args a) {
     constexpr int R = 32 * KS;                        // K of the product
     constexpr int V = kPiece;
     __shared__ alignas(16) Stage<R> stage;
@@ -67,7 +67,9 @@ __global__ __launch_bounds__(256, KS == 4 ? 1 : 2) void wide_kernel(Args a) {
             if (t.rows <= 0) continue;
             const bool some = t.key < a.n_adapters;
             with_groups(t, [&](auto groups) {
-                constexpr int G = decltype(groups)::value, MT = G < 2 ? 1 : 2;   // groups of 16 rows, and at a time
+                // groups of 16 rows, and at a time (fp32 matrices and 128 ranks need the registers: 31.5 us with 1,
+                // 44.5 with 2, for 4096 fp32 rows at rank 16; 25.4 and 38.6 for as many bf16 rows at rank 128)
+                constexpr int G = decltype(groups)::value, MT = G < 2 || sizeof(W) == 4 || KS == 4 ? 1 : 2;
                 const X *base = (const X *)a.base;
                 const W *w = (const W *)a.m + (int64_t)t.key * a.rank * a.cols;
                 int32_t row[G][4];
