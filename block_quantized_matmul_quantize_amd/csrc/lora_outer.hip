@@ -37,7 +37,9 @@ __global__ __launch_bounds__(256) void outer_kernel(Args a) {
     constexpr int V = kCols<X, RT>, C = 16 * V, R = 16 * RT;
     __shared__ float sum[R][C + 4];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, m = lane & 15, g = lane >> 4;
-    for (int64_t item = blockIdx.x; item < a.items; item += gridDim.x) {
+    for (int64_t b = blockIdx.x; b < a.items; b += gridDim.x) {
+        // neighbouring blocks of columns on one die: they share h in its L2, and spread over its channels
+        const int64_t item = xcd_remap(b, a.items);
         // (adapter, job, block of columns, split of the rows)
         const int64_t per = (a.job[0].slices + a.job[1].slices) * a.splits;
         const int64_t c = item / per;
