@@ -1,6 +1,11 @@
 // Embedding lookup: y[i] = scale * table[ids[i]], the table rows fp32, fp16, bf16 or GGUF blocks that
 // are decoded on the way (embedding tables ship in the same block types as the weights), and its
 // gradient: dT[v] = scale * (sum of dy[i] over the tokens with id v), over tokens sorted by id.
+//
+// The lookup reads each named row's bytes and writes y, a few operations a value: launch latency bounds
+// a step's 8 tokens (3 us), HBM the large calls (2048 rows of 4096 Q6_K values into fp32: 11 us, 40 MB
+// at 3.7 TB/s, 83 % of it the output).  A thread decodes 8 neighbouring values, so that it stores 16
+// or 32 bytes and finds their scale once.
 #include "common.hpp"
 #include "launch.hpp"
 #include "rowtypes.hpp"

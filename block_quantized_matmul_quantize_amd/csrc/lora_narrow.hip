@@ -7,6 +7,9 @@
 // values of all its rows, read straight into the operand registers of the matrix instructions (nothing
 // is read twice within a workgroup, so LDS would serve no reuse), several steps in flight.  The waves'
 // sums meet in LDS, in a fixed order.
+//
+// 2048 rows of 4096 fp32 values at rank 16: 10.8 us (3.1 TB/s); 8192 rows of 4096 bf16 values at rank
+// 64, transposed: 24 us (2.8 TB/s); 32 rows of 64 adapters: 4.6 us.
 #include "launch.hpp"
 #include "lora_parts.hpp"
 #include "sort_rows.hpp"
@@ -170,7 +173,8 @@ __global__ __launch_bounds__(256, RT == 8 ? 1 : 2) void narrow_kernel(Args a) {
 
 int tiles_of_rank(int64_t rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
 
-// Slices of K: enough for 256 workgroups, at most 8 partial sums a result, each of 128 values or more.
+// Slices of K: enough for 256 workgroups (2048 rows: 11.5 us, 14.4 us with 512), at most 8 partial sums a
+// result (32 rows: 6.5 us in the second half, 7.0 us with 16), each of 128 values or more.
 int slices_of(int64_t n, int64_t k) {
     const int64_t steps = (k + 127) / 128, windows = (n + kWindow - 1) / kWindow;
     int64_t s = 256 / windows;

