@@ -38,7 +38,7 @@ struct Narrow {
     static constexpr bool kNat = kNative<X, W>;
     typedef Step<X, W, MT, RT, KM> S;
     const X *x[MT];         // the lane's rows, at its group's first K value
-    const W *w;             // KM: m[c], row RT * (lane % 16); else m[c] at column RT * (lane % 16)
+    const W *w;             // KM: m[c], row r0; else m[c] at column r0
     int64_t k, rank;
     int g8, r0;
 
@@ -47,20 +47,21 @@ struct Narrow {
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
             if constexpr (TAIL) s.x[t] = load8<XV>(x[t] + kk, left);
-            else s.x[t] = load8(x[t] + kk);
+            else s.x[t] = XV ? load8(x[t] + kk) : load8_any(x[t] + kk);
         }
         if constexpr (KM) {
 #pragma unroll
             for (int q = 0; q < RT; ++q) {   // ranks past the last repeat it: their sums are not used
                 const W *p = w + (r0 + q < rank ? q : rank - 1 - r0) * k + kk + g8;
                 if constexpr (TAIL) s.w[q] = load8<WV>(p, left);
-                else s.w[q] = load8(p);
+                else s.w[q] = WV ? load8(p) : load8_any(p);
             }
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 if (!TAIL || e < left) {
-                    s.w[0].row[e] = load_row<WV, RT>(w + (kk + g8 + e) * rank, (int)(rank - r0));
+                    const W *p = w + (kk + g8 + e) * rank;
+                    s.w[0].row[e] = WV ? load_row<true, RT>(p, RT) : load_any<RT>(p);
                 } else {
 #pragma unroll
                     for (int q = 0; q < RT; ++q) s.w[0].row[e].v[q] = (W)0.f;
@@ -87,21 +88,19 @@ struct Narrow {
         // steps whose loads are in flight together: 8 to 16 KB a wave
         constexpr int U = RT >= 4 ? (RT == 8 || MT == 4 ? 1 : 2) : MT == 4 ? 2 : 4;
         int64_t kk = lo;
-        if constexpr (XV && (WV || !KM)) {
-            for (; kk + 128 * (U - 1) + 32 <= hi; kk += 128 * U) {
-                S s[U];
+        for (; kk + 128 * (U - 1) + 32 <= hi; kk += 128 * U) {
+            S s[U];
 #pragma unroll
-                for (int u = 0; u < U; ++u) load<false>(s[u], kk + 128 * u);
+            for (int u = 0; u < U; ++u) load<false>(s[u], kk + 128 * u);
 #pragma unroll
-                for (int u = 0; u < U; ++u) add(s[u], acc);
-            }
-            if constexpr (U > 1)
-                for (; kk + 32 <= hi; kk += 128) {
-                    S s;
-                    load<false>(s, kk);
-                    add(s, acc);
-                }
+            for (int u = 0; u < U; ++u) add(s[u], acc);
         }
+        if constexpr (U > 1)
+            for (; kk + 32 <= hi; kk += 128) {
+                S s;
+                load<false>(s, kk);
+                add(s, acc);
+            }
         for (; kk < hi; kk += 128) {
             S s;
             load<true>(s, kk);
@@ -135,8 +134,10 @@ __global__ __launch_bounds__(256, RT == 8 ? 1 : 2) void narrow_kernel(Args a) {
                 op.k = a.k;
                 op.rank = a.rank;
                 op.g8 = 8 * g;
-                op.r0 = RT * m < a.rank ? RT * m : a.rank - 1;
-                if (WV && !KM && op.r0 + RT > a.rank) op.r0 = a.rank - RT;
+                // ranks past the last repeat valid ones: KM the last, else the last RT, so that a piece of ranks
+                // lies within its row; of a rank that is no multiple of RT, those below `own` are another lane's
+                op.r0 = KM ? (RT * m < a.rank ? RT * m : a.rank - 1) : (RT * m + RT <= a.rank ? RT * m : a.rank - RT);
+                const int own = RT * m - op.r0;
 #pragma unroll
                 for (int u = 0; u < MT; ++u) op.x[u] = (const X *)a.v + (i0 + t.row(16 * u + m)) * a.k + op.g8;
                 op.w = (const W *)a.m + (int64_t)t.key * a.rank * a.k + (KM ? op.r0 * a.k : op.r0);
@@ -155,7 +156,8 @@ __global__ __launch_bounds__(256, RT == 8 ? 1 : 2) void narrow_kernel(Args a) {
                             for (int e = 0; e < 4; ++e)
 #pragma unroll
                                 for (int q = 0; q < RT; ++q) {
-                                    float *p = &red[16 * u + 4 * g + e][RT * m + q];
+                                    if (!KM && !WV && q < own) continue;
+                                    float *p = &red[16 * u + 4 * g + e][KM || WV ? RT * m + q : op.r0 + q];
                                     *p = w ? *p + acc[u][q][e] : acc[u][q][e];
                                 }
                     __syncthreads();

@@ -32,7 +32,7 @@ struct Args {
     const int32_t *order, *bounds;
     float *part;            // [splits][n_adapters * rank * (all columns)], where splits > 1
     int64_t items, out_total;
-    int32_t rank, splits, n_adapters;
+    int32_t rank, splits, n_adapters, spread;
 };
 
 template <class X, int RT> constexpr int kCols = sizeof(X) == 4 || RT == 8 ? 4 : 8;   // a lane's columns
@@ -53,21 +53,24 @@ __global__ __launch_bounds__(256) void outer_kernel(Args a) {
         u /= a.splits;
         const int which = u < a.job[0].slices ? 0 : 1;
         const Job &job = a.job[which];
-        const int64_t col0 = (which ? u - a.job[0].slices : u) * C;
+        // spread: a block of columns for each wave
+        const int64_t block = which ? u - a.job[0].slices : u;
+        const int64_t col0 = (a.spread ? 4 * block + wave : block) * C;
         const int64_t lo = a.bounds[c], hi = a.bounds[c + 1];
         const X *v = (const X *)job.v;
         // columns and ranks past the last repeat valid ones: their sums are not used
         const int64_t left = job.cols - col0 - V * m;
         const int64_t col = left >= V || (!VV && left > 0) ? col0 + V * m : VV ? job.cols - V : job.cols - 1;
         const int nc = left >= V ? V : left > 0 ? (int)left : VV ? V : 1;
+        const bool whole = __ballot(nc != V) == 0;
         f32x4 acc[RT][V];
 #pragma unroll
         for (int p = 0; p < RT; ++p)
 #pragma unroll
             for (int q = 0; q < V; ++q) acc[p][q] = f32x4{0.f, 0.f, 0.f, 0.f};
         // steps at multiples of 32 places; an adapter without rows has none (its lo may be past the last row)
-        const int64_t step = (int64_t)a.splits * 4 * 32;
-        const int64_t start = lo < hi ? lo / 32 * 32 + (split * 4 + wave) * 32 : hi;
+        const int64_t step = a.spread ? 32 : (int64_t)a.splits * 4 * 32;
+        const int64_t start = lo < hi && col0 < job.cols ? lo / 32 * 32 + (a.spread ? 0 : (split * 4 + wave) * 32) : hi;
         auto rows_of = [&](int64_t p0) {   // lane l: row of place p0 + l % 32 (of a place of the adapter, at the ends)
             const int64_t at = p0 + (lane & 31);
             return a.order[at < lo ? lo : at < hi ? at : hi - 1];
@@ -76,10 +79,15 @@ __global__ __launch_bounds__(256) void outer_kernel(Args a) {
         for (int64_t p0 = start; p0 < hi; p0 += step) {
             Rows8<X, V> xs;
             Frag<3> hf[RT];
+            const X *at_row[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int64_t i = __shfl(rows, 8 * g + e);
-                xs.row[e] = load_row<VV, V>(v + i * job.cols + col, nc);
+            for (int e = 0; e < 8; ++e) at_row[e] = v + (int64_t)__shfl(rows, 8 * g + e) * job.cols + col;
+            if (VV || whole) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) xs.row[e] = VV ? load_row<true, V>(at_row[e], V) : load_any<V>(at_row[e]);
+            } else {   // the last block of columns
+#pragma unroll
+                for (int e = 0; e < 8; ++e) xs.row[e] = load_row<false, V>(at_row[e], nc);
             }
             rows = rows_of(p0 + step);   // the next step's, in flight during this one
 #pragma unroll
@@ -112,6 +120,28 @@ __global__ __launch_bounds__(256) void outer_kernel(Args a) {
             }
         }
         // acc[p][q] element e: rank 16 * p + 4g + e, column col0 + V * m + q
+        if (a.spread) {
+            const float scale = job.scale ? job.scale[c] : 1.f;
+            float *out = job.out + c * a.rank * job.cols;
+#pragma unroll
+            for (int p = 0; p < RT; ++p) {
+                const int r = 16 * p + 4 * g;
+#pragma unroll
+                for (int q = 0; q < V; ++q) {
+                    const int64_t k = col0 + V * m + q;
+                    if (k >= job.cols) continue;
+                    f32x4 o = acc[p][q] * scale;
+                    if (!job.by_row && r + 4 <= a.rank) {
+                        __builtin_memcpy(out + k * a.rank + r, &o, sizeof(o));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (r + e < a.rank) out[job.by_row ? (r + e) * job.cols + k : k * a.rank + r + e] = o[e];
+                    }
+                }
+            }
+            continue;
+        }
         for (int w = 0; w < 4; ++w) {
             if (wave == w) {
 #pragma unroll
@@ -164,6 +194,10 @@ int splits_of(int64_t n, int64_t n_adapters, int64_t blocks) {
     if (s > most) s = most;
     return s < 1 ? 1 : s > 16 ? 16 : (int)s;
 }
+// With few rows an adapter the four waves of a workgroup take a block of columns each instead of steps of
+// rows that are not there (157 rows of 57 adapters at rank 64, 4625 columns: 36 us, 51 us with steps; from
+// 64 rows an adapter on, every wave has a step or two of its own).
+bool spread_of(int64_t n, int64_t n_adapters) { return n / n_adapters < 64; }
 int rank_tiles(int64_t rank) { return lora_padded_rank(rank) / 16; }
 int64_t block_cols(int x_type, int rt) { return x_type == kF32 || rt == 8 ? 64 : 128; }
 int64_t blocks_of(int x_type, int64_t rank, int64_t cols) {
@@ -179,7 +213,7 @@ size_t lora_outer_bytes(int64_t n, int64_t k, int64_t rows, int64_t rank, int64_
     for (int which = 1; which < 4; ++which) {
         const int64_t c = (which & 1 ? k : 0) + (which & 2 ? rows : 0);
         const int64_t blocks = (which & 1 ? blocks_of(kBF16, rank, k) : 0) + (which & 2 ? blocks_of(kBF16, rank, rows) : 0);
-        const int s = splits_of(n, n_adapters, blocks);
+        const int s = spread_of(n, n_adapters) ? 1 : splits_of(n, n_adapters, blocks);
         const size_t bytes = s > 1 ? (size_t)s * n_adapters * rank * c * 4 : 0;
         if (bytes > most) most = bytes;
     }
@@ -200,11 +234,13 @@ hipError_t launch_lora_outer(int x_type, const void *x, const uint16_t *parts_dh
     a.n_adapters = (int32_t)n_adapters;
     const int rt = rank_tiles(rank);
     int64_t blocks = 0;
+    a.spread = spread_of(n, n_adapters);
     for (Job &j : a.job) {
         j.slices = blocks_of(x_type, rank, j.cols);
+        if (a.spread) j.slices = (j.slices + 3) / 4;
         blocks += j.slices;
     }
-    a.splits = splits_of(n, n_adapters, blocks);
+    a.splits = a.spread ? 1 : splits_of(n, n_adapters, blocks);
     a.items = n_adapters * blocks * a.splits;
     a.out_total = n_adapters * rank * (a.job[0].cols + a.job[1].cols);
     hipError_t e = with_type(x_type, [&](auto t) -> hipError_t {

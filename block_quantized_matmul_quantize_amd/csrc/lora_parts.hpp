@@ -246,7 +246,16 @@ template <bool VEC, class T> __device__ __forceinline__ Raw8<T> load8(const T *p
     return r;
 }
 
-// The same without a limit.
+// N elements at any multiple of their size: still 16 bytes a load, which gfx950 takes at any address.
+template <int N, class T> __device__ __forceinline__ Piece<T, N> load_any(const T *p) {
+    Piece<T, N> r;
+    __builtin_memcpy(&r, p, sizeof(r));
+    return r;
+}
+template <class T> __device__ __forceinline__ Raw8<T> load8_any(const T *p) {
+    return __builtin_bit_cast(Raw8<T>, load_any<8>(p));
+}
+// Eight aligned elements, all the row's own.
 template <class T> __device__ __forceinline__ Raw8<T> load8(const T *p) {
     return __builtin_bit_cast(Raw8<T>, *(const Piece<T, 8> *)p);
 }
@@ -281,6 +290,7 @@ template <bool VEC, int N, class T> __device__ __forceinline__ Piece<T, N> load_
     if constexpr (VEC || N == 1) {
         return *(const Piece<T, N> *)p;
     } else {
+        if (left >= N) return load_any<N>(p);
         Piece<T, N> r;
 #pragma unroll
         for (int q = 0; q < N; ++q) r.v[q] = p[q < left ? q : left - 1];

@@ -88,10 +88,21 @@ __global__ __launch_bounds__(256, KS == 4 && sizeof(W) == 4 ? 1 : 2) void wide_k
                 Piece<X, V> b[MT][4];
                 auto load_base = [&](int64_t at, int u0) {
                     const int64_t col = col_of(at);
+                    if (OV || at + 16 * V <= hi) {
 #pragma unroll
-                    for (int u = 0; u < MT; ++u)
+                        for (int u = 0; u < MT; ++u)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) b[u][e] = load_row<OV, V>(base + row[u0 + u][e] * a.cols + col, width_of(col));
+                            for (int e = 0; e < 4; ++e) {
+                                const X *p = base + row[u0 + u][e] * a.cols + col;
+                                b[u][e] = OV ? load_row<true, V>(p, V) : load_any<V>(p);
+                            }
+                    } else {   // the last columns
+#pragma unroll
+                        for (int u = 0; u < MT; ++u)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                b[u][e] = load_row<false, V>(base + row[u0 + u][e] * a.cols + col, width_of(col));
+                    }
                 };
                 int64_t c0 = lo + wave * (16 * V);
                 if (base && c0 < hi) load_base(c0, 0);
@@ -199,6 +210,8 @@ __global__ __launch_bounds__(256, KS == 4 && sizeof(W) == 4 ? 1 : 2) void wide_k
                                 X *p = (X *)a.out + row[u0 + u][e] * a.cols + col;
                                 if constexpr (OV) {
                                     *(Piece<X, V> *)p = o;
+                                } else if (nw == V) {
+                                    __builtin_memcpy(p, &o, sizeof(o));
                                 } else {
 #pragma unroll
                                     for (int q = 0; q < V; ++q)
