@@ -92,6 +92,8 @@ _sig("qmm_sort_ids", _i32, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp)
 _sig("qmm_gather_sorted", _i32, _i32, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp)
 _sig("qmm_combine", _i32, _i32, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp)
 _sig("qmm_combine_backward", _i32, _i32, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp)
+_sig("qmm_combine_ids", _i32, _i32, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp)
+_sig("qmm_combine_ids_backward", _i32, _i32, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp)
 _sig("qmm_embed", _i32, _i32, _vp, _i64, _i64, _vp, _i64, ctypes.c_float, _i32, _vp, _vp)
 _sig("qmm_embed_backward_workspace", _sz, _i64, _i64, _i64)
 _sig("qmm_embed_backward", _i32, _i32, _vp, _i64, _i64, _vp, _i64, ctypes.c_float, _i32, _vp, _vp, _sz, _vp)
@@ -665,12 +667,25 @@ def gather_sorted(x, pos, bounds, out=None):
     return out
 
 
-def combine(h, pos=None, weights=None, base=None, out=None):
+def _pair_ids(ids, n_exp, shape):
+    """Address of matmul_id's ids [n_tok, top_k] (None: a null pointer)."""
+    if ids is None:
+        return None
+    if n_exp is None or n_exp < 1:
+        raise ValueError(f"n_exp must be >= 1 beside ids, got {n_exp}")
+    return _arg(ids, torch.int32, shape, "ids")
+
+
+def combine(h, pos=None, weights=None, base=None, out=None, ids=None, n_exp=None):
     """out[t] = base[t] + sum over j of weights[t, j] * h[pos[t, j]].  h: [n_tok * top_k, k] in expert
     order with pos int32 [n_tok, top_k] (entries outside the rows add nothing), or, without pos, in
-    (token, slot) order [n_tok, top_k, k] as matmul_id returns it.  weights: fp32 [n_tok, top_k]
-    (None: ones); base: [n_tok, k] or None; out may be base."""
+    (token, slot) order [n_tok, top_k, k] as matmul_id returns it.  There ids and n_exp are matmul_id's:
+    pairs whose id is outside [0, n_exp), whose rows it leaves as they were, add nothing; without ids
+    every row counts.  weights: fp32 [n_tok, top_k] (None: ones); base: [n_tok, k] or None; out may be
+    base."""
     e = _elem(h, "h")
+    if ids is not None and pos is not None:
+        raise ValueError("ids are of h in (token, slot) order, without pos")
     if pos is None:
         if h.dim() != 3 or h.shape[1] < 1:
             raise ValueError("h must be 3-D [n_tok, top_k, k] where pos is None")
@@ -682,23 +697,30 @@ def combine(h, pos=None, weights=None, base=None, out=None):
         if h.dim() != 2 or h.shape[0] != n_tok * top_k:
             raise ValueError(f"h must be [{n_tok * top_k}, k]")
         k = h.shape[1]
+    pi = _pair_ids(ids, n_exp, (n_tok, top_k))
     pw = _arg(weights, torch.float32, (n_tok, top_k), "weights")
     pb = _arg(base, h.dtype, (n_tok, k), "base")
     po = _arg(out, h.dtype, (n_tok, k), "out")
-    _same_device(h, pos, weights, base, out)
+    _same_device(h, pos, weights, base, out, ids)
     if out is None:
         out = h.new_empty((n_tok, k))
         po = out.data_ptr()
-    st = _L.qmm_combine(e, h.data_ptr(), n_tok, top_k, k, pp, pw, pb, po, _stream())
+    if ids is None:
+        st = _L.qmm_combine(e, h.data_ptr(), n_tok, top_k, k, pp, pw, pb, po, _stream())
+    else:
+        st = _L.qmm_combine_ids(e, h.data_ptr(), n_tok, top_k, k, pi, n_exp, pw, pb, po, _stream())
     if st:
         _check(st)
     return out
 
 
-def combine_backward(dy, h, pos=None, weights=None, bounds=None):
+def combine_backward(dy, h, pos=None, weights=None, bounds=None, ids=None, n_exp=None):
     """Gradient of combine: (dh of h's shape and dtype, fp32 dw [n_tok, top_k]); dy [n_tok, k].  With pos,
-    bounds is sort_ids' (rows of dh past the valid pairs are zeros).  The gradient of base is dy."""
+    bounds is sort_ids' (rows of dh past the valid pairs are zeros).  With ids and n_exp, dh and dw of a
+    pair whose id is outside [0, n_exp) are zeros.  The gradient of base is dy."""
     e = _elem(h, "h")
+    if ids is not None and pos is not None:
+        raise ValueError("ids are of h in (token, slot) order, without pos")
     if pos is None:
         if h.dim() != 3 or h.shape[1] < 1:
             raise ValueError("h must be 3-D [n_tok, top_k, k] where pos is None")
@@ -711,12 +733,18 @@ def combine_backward(dy, h, pos=None, weights=None, bounds=None):
             raise ValueError(f"h must be [{n_tok * top_k}, k]")
         k = h.shape[1]
         nv = _valid_count(bounds)
+    pi = _pair_ids(ids, n_exp, (n_tok, top_k))
     pd = _arg(dy, h.dtype, (n_tok, k), "dy")
     pw = _arg(weights, torch.float32, (n_tok, top_k), "weights")
-    _same_device(h, dy, pos, weights, bounds)
+    _same_device(h, dy, pos, weights, bounds, ids)
     dh = torch.empty_like(h)
     dw = h.new_empty((n_tok, top_k), dtype=torch.float32)
-    st = _L.qmm_combine_backward(e, pd, h.data_ptr(), n_tok, top_k, k, pp, pw, nv, dh.data_ptr(), dw.data_ptr(), _stream())
+    if ids is None:
+        st = _L.qmm_combine_backward(e, pd, h.data_ptr(), n_tok, top_k, k, pp, pw, nv, dh.data_ptr(), dw.data_ptr(),
+                                     _stream())
+    else:
+        st = _L.qmm_combine_ids_backward(e, pd, h.data_ptr(), n_tok, top_k, k, pi, n_exp, pw, dh.data_ptr(),
+                                         dw.data_ptr(), _stream())
     if st:
         _check(st)
     return dh, dw

@@ -78,6 +78,33 @@ qmm_status need_pairs(int type, int64_t n_tok, int64_t top_k, int64_t k) {
     return QMM_OK;
 }
 
+// Both forms of the combine: pos of places, or of ids in [0, n_ids).
+qmm_status need_ids(const int32_t *ids, int64_t n_ids, int64_t n_tok) {
+    TRY(need_count(n_ids, 1, "n_ids"));
+    return ids || n_tok == 0 ? QMM_OK : fail(QMM_ERR_ARG, "null ids");
+}
+qmm_status combine(int type, const void *h, int64_t n_tok, int64_t top_k, int64_t k, const int32_t *pos,
+                   int64_t n_ids, const float *w, const void *base, void *y, void *stream, const char *what) {
+    if (n_tok == 0) return QMM_OK;
+    if (!h || !y) return fail(QMM_ERR_ARG, "null h or y");
+    if (h == y) return fail(QMM_ERR_ARG, "y must not be h");
+    if (!at(h, elem(type)) || !at(y, elem(type)) || !at(base, elem(type)) || !at(pos, 4) || !at(w, 4))
+        return fail(QMM_ERR_ARG, "h, y, base, w and the places or ids must be aligned to their elements");
+    return done(qmm::launch_combine(type, h, n_tok, top_k, k, pos, n_ids, w, base, y, (hipStream_t)stream), what);
+}
+qmm_status combine_backward(int type, const void *dy, const void *h, int64_t n_tok, int64_t top_k, int64_t k,
+                            const int32_t *pos, int64_t n_ids, const float *w, const int32_t *n_valid, void *dh,
+                            float *dw, void *stream, const char *what) {
+    if (n_tok == 0) return QMM_OK;
+    if (!dy || !h || !dh || !dw) return fail(QMM_ERR_ARG, "null dy, h, dh or dw");
+    if (dh == dy || dh == h) return fail(QMM_ERR_ARG, "dh must not be dy or h");
+    if (!at(dy, elem(type)) || !at(h, elem(type)) || !at(dh, elem(type)) || !at(pos, 4) || !at(w, 4) || !at(dw, 4) ||
+        !at(n_valid, 4))
+        return fail(QMM_ERR_ARG, "dy, h, dh, dw, w, n_valid and the places or ids must be aligned to their elements");
+    return done(qmm::launch_combine_backward(type, dy, h, n_tok, top_k, k, pos, n_ids, w, n_valid, dh, dw,
+                                             (hipStream_t)stream), what);
+}
+
 qmm_status need_lora(int64_t n, int64_t k, int64_t rows, int64_t rank, int64_t n_adapters) {
     TRY(need_count(n, 0, "n"));
     TRY(need_len(k, "k"));
@@ -133,26 +160,31 @@ qmm_status qmm_gather_sorted(int type, const void *x, int64_t n_tok, int64_t top
 qmm_status qmm_combine(int type, const void *h, int64_t n_tok, int64_t top_k, int64_t k, const int32_t *pos,
                        const float *w, const void *base, void *y, void *stream) {
     TRY(need_pairs(type, n_tok, top_k, k));
-    if (n_tok == 0) return QMM_OK;
-    if (!h || !y) return fail(QMM_ERR_ARG, "null h or y");
-    if (h == y) return fail(QMM_ERR_ARG, "y must not be h");
-    if (!at(h, elem(type)) || !at(y, elem(type)) || !at(base, elem(type)) || !at(pos, 4) || !at(w, 4))
-        return fail(QMM_ERR_ARG, "h, y, base, pos and w must be aligned to their elements");
-    return done(qmm::launch_combine(type, h, n_tok, top_k, k, pos, w, base, y, (hipStream_t)stream), "qmm_combine");
+    return combine(type, h, n_tok, top_k, k, pos, 0, w, base, y, stream, "qmm_combine");
+}
+
+qmm_status qmm_combine_ids(int type, const void *h, int64_t n_tok, int64_t top_k, int64_t k, const int32_t *ids,
+                           int64_t n_ids, const float *w, const void *base, void *y, void *stream) {
+    TRY(need_pairs(type, n_tok, top_k, k));
+    TRY(need_ids(ids, n_ids, n_tok));
+    return combine(type, h, n_tok, top_k, k, ids, n_ids, w, base, y, stream, "qmm_combine_ids");
 }
 
 qmm_status qmm_combine_backward(int type, const void *dy, const void *h, int64_t n_tok, int64_t top_k, int64_t k,
                                 const int32_t *pos, const float *w, const int32_t *n_valid, void *dh, float *dw,
                                 void *stream) {
     TRY(need_pairs(type, n_tok, top_k, k));
-    if (n_tok == 0) return QMM_OK;
-    if (!dy || !h || !dh || !dw || (pos && !n_valid)) return fail(QMM_ERR_ARG, "null dy, h, dh, dw or n_valid");
-    if (dh == dy || dh == h) return fail(QMM_ERR_ARG, "dh must not be dy or h");
-    if (!at(dy, elem(type)) || !at(h, elem(type)) || !at(dh, elem(type)) || !at(pos, 4) || !at(w, 4) || !at(dw, 4) ||
-        !at(n_valid, 4))
-        return fail(QMM_ERR_ARG, "dy, h, dh, dw, pos, w and n_valid must be aligned to their elements");
-    return done(qmm::launch_combine_backward(type, dy, h, n_tok, top_k, k, pos, w, n_valid, dh, dw,
-                                             (hipStream_t)stream), "qmm_combine_backward");
+    if (n_tok > 0 && pos && !n_valid) return fail(QMM_ERR_ARG, "null n_valid");
+    return combine_backward(type, dy, h, n_tok, top_k, k, pos, 0, w, n_valid, dh, dw, stream, "qmm_combine_backward");
+}
+
+qmm_status qmm_combine_ids_backward(int type, const void *dy, const void *h, int64_t n_tok, int64_t top_k, int64_t k,
+                                    const int32_t *ids, int64_t n_ids, const float *w, void *dh, float *dw,
+                                    void *stream) {
+    TRY(need_pairs(type, n_tok, top_k, k));
+    TRY(need_ids(ids, n_ids, n_tok));
+    return combine_backward(type, dy, h, n_tok, top_k, k, ids, n_ids, w, nullptr, dh, dw, stream,
+                            "qmm_combine_ids_backward");
 }
 
 qmm_status qmm_embed(int type, const void *table, int64_t vocab, int64_t k, const int32_t *ids, int64_t n, float scale,

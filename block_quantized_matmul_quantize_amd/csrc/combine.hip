@@ -38,10 +38,19 @@ __global__ __launch_bounds__(256) void gather_kernel(const E *__restrict__ x, in
     }
 }
 
+// Row of h of pair q, -1 for none.  pos: the row of each pair; with n_ids > 0 the id of each pair, whose row
+// is the q-th and counts only where the id is in [0, n_ids); null: the q-th.
+__device__ __forceinline__ int64_t row_of(const int32_t *pos, int64_t n_ids, int64_t q, int64_t pairs) {
+    if (!pos) return q;
+    const int64_t p = pos[q];
+    if (n_ids) return p >= 0 && p < n_ids ? q : -1;
+    return p >= 0 && p < pairs ? p : -1;
+}
+
 template <class E, int N>
 __global__ __launch_bounds__(256) void combine_kernel(const E *__restrict__ h, int64_t n_tok, int64_t top_k, int64_t k,
-                                                      const int32_t *__restrict__ pos, const float *__restrict__ w,
-                                                      const E *base, E *y) {
+                                                      const int32_t *__restrict__ pos, int64_t n_ids,
+                                                      const float *__restrict__ w, const E *base, E *y) {
     const int64_t col = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * N;
     if (col >= k) return;
     const int64_t pairs = n_tok * top_k;
@@ -50,8 +59,8 @@ __global__ __launch_bounds__(256) void combine_kernel(const E *__restrict__ h, i
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[i] = 0.f;
         for (int64_t j = 0; j < top_k; ++j) {
-            const int64_t q = t * top_k + j, p = pos ? pos[q] : q;
-            if (p < 0 || p >= pairs) continue;
+            const int64_t q = t * top_k + j, p = row_of(pos, n_ids, q, pairs);
+            if (p < 0) continue;
             const float c = w ? w[q] : 1.f;
             load_n<N>(h + p * k + col, v);
 #pragma unroll
@@ -70,16 +79,17 @@ __global__ __launch_bounds__(256) void combine_kernel(const E *__restrict__ h, i
 template <class E, int N>
 __global__ __launch_bounds__(256) void combine_backward_kernel(const E *__restrict__ dy, const E *__restrict__ h,
                                                                int64_t n_tok, int64_t top_k, int64_t k,
-                                                               const int32_t *__restrict__ pos,
+                                                               const int32_t *__restrict__ pos, int64_t n_ids,
                                                                const float *__restrict__ w,
                                                                const int32_t *__restrict__ n_valid,
                                                                E *__restrict__ dh, float *__restrict__ dw) {
     __shared__ float sums[4];
     const int64_t pairs = n_tok * top_k;
     for (int64_t q = blockIdx.x; q < pairs; q += gridDim.x) {
-        const int64_t t = q / top_k, p = pos ? pos[q] : q;
-        const bool ok = p >= 0 && p < pairs;
-        if (pos && q >= *n_valid)
+        const int64_t t = q / top_k, p = row_of(pos, n_ids, q, pairs);
+        const bool ok = p >= 0;
+        // dh's q-th row: the pair's own, or one past the valid places
+        if (n_ids ? !ok : pos && q >= *n_valid)
             for (int64_t col = threadIdx.x * N; col < k; col += 256 * N) {
                 float z[N];
 #pragma unroll
@@ -136,26 +146,26 @@ hipError_t launch_gather_sorted(int type, const void *x, int64_t n_tok, int64_t 
 }
 
 hipError_t launch_combine(int type, const void *h, int64_t n_tok, int64_t top_k, int64_t k, const int32_t *pos,
-                          const float *w, const void *base, void *y, hipStream_t s) {
+                          int64_t n_ids, const float *w, const void *base, void *y, hipStream_t s) {
     return with_type(type, [&](auto e) -> hipError_t {
         typedef decltype(e) E;
         constexpr int N = 16 / sizeof(E);
         if (k % N == 0 && aligned16(h, base, y)) {
             const int th = threads_of(k / N);
             hipLaunchKernelGGL((combine_kernel<E, N>), grid_of(n_tok, k / N, th), dim3(th), 0, s, (const E *)h, n_tok,
-                               top_k, k, pos, w, (const E *)base, (E *)y);
+                               top_k, k, pos, n_ids, w, (const E *)base, (E *)y);
         } else {
             const int th = threads_of(k);
             hipLaunchKernelGGL((combine_kernel<E, 1>), grid_of(n_tok, k, th), dim3(th), 0, s, (const E *)h, n_tok,
-                               top_k, k, pos, w, (const E *)base, (E *)y);
+                               top_k, k, pos, n_ids, w, (const E *)base, (E *)y);
         }
         return hipGetLastError();
     });
 }
 
 hipError_t launch_combine_backward(int type, const void *dy, const void *h, int64_t n_tok, int64_t top_k, int64_t k,
-                                   const int32_t *pos, const float *w, const int32_t *n_valid, void *dh, float *dw,
-                                   hipStream_t s) {
+                                   const int32_t *pos, int64_t n_ids, const float *w, const int32_t *n_valid,
+                                   void *dh, float *dw, hipStream_t s) {
     return with_type(type, [&](auto e) -> hipError_t {
         typedef decltype(e) E;
         constexpr int N = 16 / sizeof(E);
@@ -163,10 +173,10 @@ hipError_t launch_combine_backward(int type, const void *dy, const void *h, int6
         const dim3 grid((unsigned)(pairs < 1 << 20 ? pairs : 1 << 20));
         if (k % N == 0 && aligned16(dy, h, dh))
             hipLaunchKernelGGL((combine_backward_kernel<E, N>), grid, dim3(256), 0, s, (const E *)dy, (const E *)h,
-                               n_tok, top_k, k, pos, w, n_valid, (E *)dh, dw);
+                               n_tok, top_k, k, pos, n_ids, w, n_valid, (E *)dh, dw);
         else
             hipLaunchKernelGGL((combine_backward_kernel<E, 1>), grid, dim3(256), 0, s, (const E *)dy, (const E *)h,
-                               n_tok, top_k, k, pos, w, n_valid, (E *)dh, dw);
+                               n_tok, top_k, k, pos, n_ids, w, n_valid, (E *)dh, dw);
         return hipGetLastError();
     });
 }

@@ -162,11 +162,12 @@ hipError_t launch_sort_ids(const int32_t *ids, int64_t n, int64_t n_keys, int32_
                            int32_t *bounds, bool with_keys, uint8_t *ws, hipStream_t s);
 hipError_t launch_gather_sorted(int type, const void *x, int64_t n_tok, int64_t top_k, int64_t k, const int32_t *pos,
                                 const int32_t *n_valid, void *y, hipStream_t s);
+// pos: places, null for (token, slot) order, or with n_ids > 0 the ids of pairs in that order.
 hipError_t launch_combine(int type, const void *h, int64_t n_tok, int64_t top_k, int64_t k, const int32_t *pos,
-                          const float *w, const void *base, void *y, hipStream_t s);
+                          int64_t n_ids, const float *w, const void *base, void *y, hipStream_t s);
 hipError_t launch_combine_backward(int type, const void *dy, const void *h, int64_t n_tok, int64_t top_k, int64_t k,
-                                   const int32_t *pos, const float *w, const int32_t *n_valid, void *dh, float *dw,
-                                   hipStream_t s);
+                                   const int32_t *pos, int64_t n_ids, const float *w, const int32_t *n_valid,
+                                   void *dh, float *dw, hipStream_t s);
 hipError_t launch_embed(int type, const void *table, int64_t vocab, int64_t k, const int32_t *ids, int64_t n,
                         float scale, int y_type, void *y, hipStream_t s);
 size_t embed_backward_bytes(int64_t n, int64_t k, int64_t vocab);

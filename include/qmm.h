@@ -264,11 +264,16 @@ qmm_status qmm_matmul_id_glu(int type, const void *w_gate, const void *w_up, int
  *   gradient is qmm_combine without weights.
  * qmm_combine: and back: y[t] = base[t] + sum over j of w[t][j] * h[pos[t][j]].  h [n_tok * top_k][k];
  *   pos int32 [n_tok][top_k], entries outside [0, n_tok * top_k) add nothing; pos NULL: h is in
- *   (token, slot) order, as qmm_matmul_id writes it.  w fp32 [n_tok][top_k], or NULL for ones;
+ *   (token, slot) order and every row of it counts.  w fp32 [n_tok][top_k], or NULL for ones;
  *   base [n_tok][k] (a shared expert's result, the residual) or NULL; y may be base.
+ * qmm_combine_ids: the same on the result of qmm_matmul_id or qmm_matmul_id_glu: h in (token, slot)
+ *   order, ids [n_tok][top_k] and n_ids (>= 1) the ids and n_exp of that call.  It has left the row of a pair
+ *   whose id is outside [0, n_ids) as it was; such a row is not read here and adds nothing.
  * qmm_combine_backward: dh[pos[t][j]] = w[t][j] * dy[t], dw[t][j] = <dy[t], h[pos[t][j]]> (fp32;
  *   0 where pos names no row); rows of dh from *n_valid on become zeros.  pos entries must differ
  *   from each other; n_valid is not read where pos is NULL.  (The gradient of base is dy.)
+ * qmm_combine_ids_backward: the gradient of qmm_combine_ids: dh[t][j] = w[t][j] * dy[t], dw[t][j] =
+ *   <dy[t], h[t][j]>, both zero for a pair whose id is outside [0, n_ids).
  * ------------------------------------------------------------------------------------------- */
 size_t qmm_sort_ids_workspace(int64_t n, int64_t n_keys);
 qmm_status qmm_sort_ids(const int32_t *ids, int64_t n, int64_t n_keys, int32_t *order, int32_t *pos,
@@ -277,9 +282,14 @@ qmm_status qmm_gather_sorted(int type, const void *x, int64_t n_tok, int64_t top
                              const int32_t *n_valid, void *y, void *stream);
 qmm_status qmm_combine(int type, const void *h, int64_t n_tok, int64_t top_k, int64_t k, const int32_t *pos,
                        const float *w, const void *base, void *y, void *stream);
+qmm_status qmm_combine_ids(int type, const void *h, int64_t n_tok, int64_t top_k, int64_t k, const int32_t *ids,
+                           int64_t n_ids, const float *w, const void *base, void *y, void *stream);
 qmm_status qmm_combine_backward(int type, const void *dy, const void *h, int64_t n_tok, int64_t top_k, int64_t k,
                                 const int32_t *pos, const float *w, const int32_t *n_valid, void *dh, float *dw,
                                 void *stream);
+qmm_status qmm_combine_ids_backward(int type, const void *dy, const void *h, int64_t n_tok, int64_t top_k, int64_t k,
+                                    const int32_t *ids, int64_t n_ids, const float *w, void *dh, float *dw,
+                                    void *stream);
 
 /* ---------------------------------------------------------------------------------------------
  * qmm_embed: y[i] = scale * table[ids[i]], zeros for an id outside [0, vocab).  table [vocab][k] of

@@ -1,0 +1,72 @@
+"""Forms of the row operators' calls on the GPU: the combine straight on the expert products' results."""
+import numpy as np
+import pytest
+import torch
+
+import block_quantized_matmul_quantize_amd as qmm
+import rows_util as ref
+import synth
+from test_gpu_rows import BF16, F16, F32, dev, gen, normal, some_ids
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------------------------------------
+# combine on (token, slot) order with ids
+# ------------------------------------------------------------------------------------------------
+def own_places(ids, n_exp):
+    """pos of pairs in (token, slot) order: the pair itself, -1 for an id outside [0, n_exp)."""
+    each = torch.arange(ids.numel(), dtype=torch.int32).view(ids.shape)
+    return torch.where((ids >= 0) & (ids < n_exp), each, torch.full_like(each, -1))
+
+
+@pytest.mark.parametrize("n,top_k", [(1, 8), (16, 8), (150, 2)])
+@pytest.mark.parametrize("stale", [7.0, float("nan")])
+def test_combine_of_matmul_id_without_its_stale_rows(n, top_k, stale):
+    """matmul_id leaves the row of a pair without an expert as it was in out; the combine with its ids does
+    not read it, and gives it no gradient."""
+    n_exp, rows, k = 10, 136, 512
+    g, r = gen(n), synth.rngs(40 + n, 2)
+    w = torch.from_numpy(np.ascontiguousarray(synth.gen_weights(qmm.Q4_K, n_exp * rows, k, r[0])))
+    ids = some_ids(g, n * top_k, n_exp, bad=0.3).view(n, top_k)
+    ids[0, 0] = -1
+    if n > 1:
+        ids[1] = torch.tensor([n_exp, -1] * (top_k // 2), dtype=torch.int32)   # a token without any expert
+    pos = own_places(ids, n_exp)
+    out = torch.full((n, top_k, rows), stale, device="cuda")
+    h, ws = qmm.matmul_id(dev(w), qmm.Q4_K, n_exp, rows, k, dev(normal(g, n, k)), dev(ids), out=out)
+    assert qmm.matmul_id_invalid_count(ws) == int((pos < 0).sum())
+    weights, base, dy = torch.rand((n, top_k), generator=g), normal(g, n, rows), normal(g, n, rows)
+    hc = h.cpu().view(-1, rows)
+    for bb in (base, None):
+        y = qmm.combine(h, None, dev(weights), base=dev(bb), ids=dev(ids), n_exp=n_exp)
+        want, mag = ref.combine(hc, pos, weights, bb)
+        ref.check(y, want, top_k + 1, mag, "combine")
+    dh, dw = qmm.combine_backward(dev(dy), h, None, dev(weights), ids=dev(ids), n_exp=n_exp)
+    wh, ww, mw = ref.combine_backward(dy, hc, pos, weights)
+    ref.check(dh, wh.view(dh.shape), 1, wh.view(dh.shape).abs(), "dh")
+    ref.check(dw, ww, rows, mw, "dw")
+    assert not dh.cpu()[pos < 0].any() and not dw.cpu()[pos < 0].any()
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("n,top_k,k", [(1, 1, 1), (5, 3, 7), (33, 10, 264), (300, 2, 1000)])
+@pytest.mark.parametrize("off", [0, 1])
+def test_combine_with_ids(n, top_k, k, dtype, off):
+    g = gen(n + k)
+    n_exp = 12
+    ids = some_ids(g, n * top_k, n_exp, bad=0.3).view(n, top_k)
+    pos = own_places(ids, n_exp)
+    h = normal(g, n * top_k, k, dtype=dtype)
+    h[pos.view(-1) < 0] = float("nan")
+    w, base, dy = torch.rand((n, top_k), generator=g), normal(g, n, k, dtype=dtype), normal(g, n, k, dtype=dtype)
+    hd, idd = dev(h.view(n, top_k, k), off), dev(ids)
+    for ww in (w, None):
+        based = dev(base, off)
+        qmm.combine(hd, None, dev(ww), base=based, out=based, ids=idd, n_exp=n_exp)
+        want, mag = ref.combine(h, pos, ww, base)
+        ref.check(based, want, top_k + 1, mag, "combine")
+        dh, dw = qmm.combine_backward(dev(dy, off), hd, None, dev(ww), ids=idd, n_exp=n_exp)
+        wh, wd, mw = ref.combine_backward(dy, h, pos, ww)
+        ref.check(dh, wh.view(dh.shape), 1, wh.view(dh.shape).abs(), "dh")
+        ref.check(dw, wd, k, mw, "dw")

@@ -1,0 +1,56 @@
+"""Refusals of the row operators' further forms, on the CPU (fake addresses: every call here ends on the host)."""
+import pytest
+import torch
+
+import block_quantized_matmul_quantize_amd as qmm
+
+P = 0x100000       # aligned to every element
+Q = P + (1 << 20)
+OK, ARG, TYPE, SHAPE = 0, -1, -2, -3
+
+
+def L():
+    return qmm.lib()
+
+
+def test_combine_with_ids_refusals():
+    def f(t=0, n=4, j=2, k=8, h=P, ids=P, ne=3, y=Q):
+        return L().qmm_combine_ids(t, h, n, j, k, ids, ne, P, P, y, None)
+
+    def b(t=0, n=4, j=2, k=8, h=P, ids=P, ne=3, y=Q):
+        return L().qmm_combine_ids_backward(t, P, h, n, j, k, ids, ne, P, y, P, None)
+
+    for call in (f, b):
+        assert call(t=12) == TYPE
+        assert call(n=-1) == ARG
+        assert call(j=0) == ARG
+        assert call(k=0) == ARG
+        assert call(k=(1 << 20) + 1) == SHAPE
+        assert call(n=1 << 29, j=4) == SHAPE
+        assert call(ne=0) == ARG
+        assert call(ne=-1) == ARG
+        assert call(ne=(1 << 30) + 1) == SHAPE
+        assert call(ids=None) == ARG
+        assert call(ids=P + 2) == ARG
+        assert call(h=None) == ARG
+        assert call(h=P + 2) == ARG
+        assert call(y=None) == ARG
+        assert call(y=P) == ARG
+        assert call(n=0, h=None, ids=None, y=None) == OK
+
+
+def test_combine_wrappers_check_ids():
+    h, ids = torch.zeros((4, 2, 16)), torch.zeros((4, 2), dtype=torch.int32)
+    for call in (lambda **a: qmm.combine(h, **a), lambda **a: qmm.combine_backward(torch.zeros((4, 16)), h, **a)):
+        with pytest.raises(ValueError, match="n_exp"):
+            call(ids=ids)
+        with pytest.raises(ValueError, match="n_exp"):
+            call(ids=ids, n_exp=0)
+        with pytest.raises(ValueError, match="ids must be"):
+            call(ids=ids[:3], n_exp=4)
+        with pytest.raises(TypeError, match="ids must have"):
+            call(ids=ids.long(), n_exp=4)
+        with pytest.raises(ValueError, match="without pos"):
+            call(pos=ids, ids=ids, n_exp=4)
+        with pytest.raises(ValueError, match="device"):
+            call(ids=ids, n_exp=4)
