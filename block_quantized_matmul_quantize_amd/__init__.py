@@ -197,9 +197,17 @@ def _torch():
     return torch
 
 
+# torch's own calls for the current device and its stream's handle: without the Stream object that
+# torch.cuda.current_stream() makes, 3 us of a call.  They are not public, so a torch without them is
+# asked through what is.
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+_get_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream():
-    # torch.cuda.current_stream() without the Stream object it makes, 3 us of a call
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    if _get_device is None or _get_raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _get_raw_stream(_get_device())
 
 
 def _need(t, dtype, name):

@@ -1,4 +1,4 @@
-"""Forms of the row operators' calls on the GPU: the combine straight on the expert products' results."""
+"""Forms of the row operators' calls on the GPU: the combine straight on the expert products' results, streams."""
 import numpy as np
 import pytest
 import torch
@@ -70,3 +70,15 @@ def test_combine_with_ids(n, top_k, k, dtype, off):
         wh, wd, mw = ref.combine_backward(dy, h, pos, ww)
         ref.check(dh, wh.view(dh.shape), 1, wh.view(dh.shape).abs(), "dh")
         ref.check(dw, wd, k, mw, "dw")
+
+
+# ------------------------------------------------------------------------------------------------
+# Streams
+# ------------------------------------------------------------------------------------------------
+def test_stream_is_torchs_current_one():
+    """By torch's own calls and by its public one, on the default stream and on another."""
+    assert qmm._stream() == torch.cuda.current_stream().cuda_stream
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        assert qmm._stream() == torch.cuda.current_stream().cuda_stream == s.cuda_stream
+    assert qmm._stream() == torch.cuda.current_stream().cuda_stream

@@ -54,3 +54,13 @@ def test_combine_wrappers_check_ids():
             call(pos=ids, ids=ids, n_exp=4)
         with pytest.raises(ValueError, match="device"):
             call(ids=ids, n_exp=4)
+
+
+@pytest.mark.parametrize("missing", ["_get_device", "_get_raw_stream"])
+def test_stream_without_torchs_private_calls(missing, monkeypatch):
+    class Stream:
+        cuda_stream = 1234
+
+    monkeypatch.setattr(qmm, missing, None)
+    monkeypatch.setattr(torch.cuda, "current_stream", Stream)
+    assert qmm._stream() == 1234
