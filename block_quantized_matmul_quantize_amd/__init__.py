@@ -597,10 +597,15 @@ def _arg(t, dtype, shape, name):
 
 
 def _same_device(first, *others):
-    """Last check before pointers cross the C ABI: every tensor lives on the first one's device."""
+    """Last check before pointers cross the C ABI: every tensor lives on the first one's device, and that is
+    the current one, on whose stream the call is enqueued."""
     dev = first.get_device()
     if dev < 0:
         raise ValueError("every tensor must be a device tensor")
+    current = torch.cuda.current_device() if _get_device is None else _get_device()
+    if dev != current:
+        raise ValueError(f"the tensors are on {first.device}, but the current device is {current}: "
+                         f"call within torch.cuda.device({dev})")
     for t in others:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"every tensor must be on {first.device}, got {t.device}")

@@ -64,3 +64,28 @@ def test_stream_without_torchs_private_calls(missing, monkeypatch):
     monkeypatch.setattr(qmm, missing, None)
     monkeypatch.setattr(torch.cuda, "current_stream", Stream)
     assert qmm._stream() == 1234
+
+
+class OnDevice:
+    """What the binding's last check asks a tensor."""
+
+    def __init__(self, index):
+        self.index, self.device = index, f"cuda:{index}"
+
+    def get_device(self):
+        return self.index
+
+
+def test_tensors_on_another_device_than_the_current_one_are_refused(monkeypatch):
+    """Their pointers would go to a kernel on the current device's stream."""
+    monkeypatch.setattr(qmm, "_get_device", lambda: 0)
+    qmm._same_device(OnDevice(0), None, OnDevice(0))
+    with pytest.raises(ValueError, match="current device is 0"):
+        qmm._same_device(OnDevice(1), OnDevice(1))
+    with pytest.raises(ValueError, match="must be on cuda:0"):
+        qmm._same_device(OnDevice(0), OnDevice(1))
+    monkeypatch.setattr(qmm, "_get_device", None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    qmm._same_device(OnDevice(1))
+    with pytest.raises(ValueError, match="current device is 1"):
+        qmm._same_device(OnDevice(0))
