@@ -766,7 +766,8 @@ def combine_backward(dy, h, pos=None, weights=None, bounds=None, ids=None, n_exp
 def embed(table, qtype, vocab, k, ids, scale=1.0, dtype=torch.float32, out=None):
     """out[i] = scale * table[ids[i]] (zeros for an id outside [0, vocab)).  table: fp32, fp16 or bf16
     [vocab, k] (qtype F32, F16, BF16), or uint8 rows of GGUF blocks; ids int32 of any shape; out
-    ids.shape + [k] of dtype.  With ids 0 .. vocab - 1 it expands a block-quantized matrix."""
+    ids.shape + [k] of dtype, from blocks at a 16-byte aligned address.  With ids 0 .. vocab - 1 it
+    expands a block-quantized matrix."""
     pi = _int32(ids, "ids")
     tt = _ELEM_DTYPES.get(qtype)
     pt = _need(table, torch.uint8 if tt is None else tt, "table")

@@ -247,8 +247,9 @@ qmm_status qmm_matmul_id_glu(int type, const void *w_gate, const void *w_up, int
  *  - ids are int32.  An id outside its range (such as -1) picks no row: padding tokens, dropped
  *    (token, slot) pairs, rows without an adapter.  Row contents that no id picks are not read into
  *    any sum, so NaN there stays there.
- *  - Pointers need the alignment of their element (QMM_ERR_ARG otherwise; blocks 2 bytes); rows of
- *    a multiple of 16 bytes at 16-byte aligned pointers are read and written faster.
+ *  - Pointers need the alignment of their element (QMM_ERR_ARG otherwise; blocks 2 bytes; the y of
+ *    qmm_embed from blocks 16 bytes).  Rows of a multiple of 16 bytes (qmm_embed: of 8 elements) at
+ *    16-byte aligned pointers are read and written faster.
  *  - Row lengths (k, rows) are 1 .. 1<<20, counts (n, n_tok * top_k) 0 .. 1<<30; longer: QMM_ERR_SHAPE.
  *    A count of 0 is a no-op, except that gradients and bounds are written as zeros.
  *  - Workspaces (ws, 256-byte aligned) need no clearing and hold nothing between calls.
@@ -294,7 +295,8 @@ qmm_status qmm_combine_ids_backward(int type, const void *dy, const void *h, int
 /* ---------------------------------------------------------------------------------------------
  * qmm_embed: y[i] = scale * table[ids[i]], zeros for an id outside [0, vocab).  table [vocab][k] of
  *   any type: elements, or rows of GGUF blocks (k a multiple of the block size), decoded as the
- *   products' weights are; y [n][k] of y_type.  With ids 0 .. vocab - 1 it expands a weight matrix.
+ *   products' weights are; y [n][k] of y_type, from blocks 16-byte aligned whatever its type (it is
+ *   written 8 values at a time).  With ids 0 .. vocab - 1 it expands a weight matrix.
  * qmm_embed_backward: grad[v] = scale * sum of dy[i] over the rows i with ids[i] = v, all vocab rows
  *   written (zeros where no id picks them).  dy [n][k] of dy_type, grad [vocab][k] of g_type.
  *   vocab <= 1<<30.

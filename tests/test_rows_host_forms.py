@@ -1,4 +1,6 @@
 """Refusals of the row operators' further forms, on the CPU (fake addresses: every call here ends on the host)."""
+import re
+
 import pytest
 import torch
 
@@ -89,3 +91,16 @@ def test_tensors_on_another_device_than_the_current_one_are_refused(monkeypatch)
     qmm._same_device(OnDevice(1))
     with pytest.raises(ValueError, match="current device is 1"):
         qmm._same_device(OnDevice(0))
+
+
+def test_embed_from_blocks_says_what_alignment_of_y_it_needs():
+    """Blocks are decoded into 8 values a store: y at less than 16 bytes is refused, and the contract says so."""
+    for y_type, size in ((qmm.F32, 4), (qmm.F16, 2), (qmm.BF16, 2)):
+        for off in (size, 8):
+            assert L().qmm_embed(qmm.Q4_K, P, 10, 256, P, 4, 1.0, y_type, P + off, None) == ARG
+    with open(qmm.HEADER) as f:
+        text = re.sub(r"[\s*]+", " ", f.read())
+    of_embed = text[text.index("qmm_embed: y[i]"):text.index("qmm_embed_backward: grad[v]")]
+    assert "from blocks 16-byte aligned" in of_embed
+    assert "from blocks 16 bytes" in text[text.index("Pointers need the alignment"):text.index("Row lengths")]
+    assert "16-byte aligned" in qmm.embed.__doc__
