@@ -553,6 +553,9 @@ def debug_subdots(w, qtype, rows, k, xq, n, path):
 
 # --------------------------------------------------------------------------------------------
 # Row operators: embedding, expert gather / combine, low-rank adapters (and their gradients)
+#
+# Like the products' calls, these are not recorded by autograd: a result requires no gradient, whatever
+# its inputs do.  A training step calls the *_backward functions itself.
 # --------------------------------------------------------------------------------------------
 _ELEM_TYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 _ELEM_DTYPES = {v: d for d, v in _ELEM_TYPES.items()}
@@ -661,7 +664,8 @@ def _need_pos(pos, name="pos"):
 
 def gather_sorted(x, pos, bounds, out=None):
     """Rows to expert order: out[pos[t, j]] = x[t] for x [n_tok, k] and sort_ids' pos [n_tok, top_k];
-    rows of out [n_tok * top_k, k] past the valid pairs are zeros.  Its gradient: combine(d_out, pos)."""
+    rows of out [n_tok * top_k, k] past the valid pairs are zeros.  Not recorded by autograd; its
+    gradient: combine(d_out, pos)."""
     e = _elem(x, "x")
     pp = _int32(pos, "pos")
     n_tok, top_k = _need_pos(pos)
@@ -695,7 +699,7 @@ def combine(h, pos=None, weights=None, base=None, out=None, ids=None, n_exp=None
     (token, slot) order [n_tok, top_k, k] as matmul_id returns it.  There ids and n_exp are matmul_id's:
     pairs whose id is outside [0, n_exp), whose rows it leaves as they were, add nothing; without ids
     every row counts.  weights: fp32 [n_tok, top_k] (None: ones); base: [n_tok, k] or None; out may be
-    base."""
+    base.  Not recorded by autograd; its gradient: combine_backward."""
     e = _elem(h, "h")
     if ids is not None and pos is not None:
         raise ValueError("ids are of h in (token, slot) order, without pos")
@@ -767,7 +771,8 @@ def embed(table, qtype, vocab, k, ids, scale=1.0, dtype=torch.float32, out=None)
     """out[i] = scale * table[ids[i]] (zeros for an id outside [0, vocab)).  table: fp32, fp16 or bf16
     [vocab, k] (qtype F32, F16, BF16), or uint8 rows of GGUF blocks; ids int32 of any shape; out
     ids.shape + [k] of dtype, from blocks at a 16-byte aligned address.  With ids 0 .. vocab - 1 it
-    expands a block-quantized matrix."""
+    expands a block-quantized matrix.  Not recorded by autograd; its gradient with respect to a table
+    of elements: embed_backward."""
     pi = _int32(ids, "ids")
     tt = _ELEM_DTYPES.get(qtype)
     pt = _need(table, torch.uint8 if tt is None else tt, "table")
@@ -840,7 +845,8 @@ def lora(x, a, b, ids, scale=None, base=None, out=None, keep_h=False, ws=None):
     """out[i] = base[i] + scale[c] * b[c] @ (a[c] @ x[i]) with c = ids[i]; base[i] alone for a c outside
     [0, n_adapters).  x [n, k] and base, out [n, rows] of one dtype; a [n_adapters, rank, k] and
     b [n_adapters, rows, rank] of x's dtype (beside fp32 x: any); ids int32 [n]; scale fp32
-    [n_adapters]; out may be base.  keep_h: returns (out, fp32 a[c] @ x[i] [n, rank]) for the backward."""
+    [n_adapters]; out may be base.  keep_h: returns (out, fp32 a[c] @ x[i] [n, rank]) for
+    lora_backward: autograd does not record the call."""
     e, w, n, k, na, rank, rows, ps = _lora_shapes(x, a, b, ids, scale)
     pb = _arg(base, x.dtype, (n, rows), "base")
     po = _arg(out, x.dtype, (n, rows), "out")

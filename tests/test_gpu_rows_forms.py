@@ -82,3 +82,23 @@ def test_stream_is_torchs_current_one():
     with torch.cuda.stream(s):
         assert qmm._stream() == torch.cuda.current_stream().cuda_stream == s.cuda_stream
     assert qmm._stream() == torch.cuda.current_stream().cuda_stream
+
+
+# ------------------------------------------------------------------------------------------------
+# Autograd
+# ------------------------------------------------------------------------------------------------
+def test_results_require_no_gradient_as_documented():
+    """The calls take inputs that require a gradient; autograd records none, and each docstring names the
+    call that computes it."""
+    g = gen(8)
+    t = [dev(normal(g, *s)).requires_grad_() for s in ((12, 32), (24, 32), (3, 8, 32), (3, 32, 8), (12, 2))]
+    x, h, a, b, w = t
+    ids = dev(torch.randint(0, 3, (12, 2), generator=g, dtype=torch.int32))
+    _, pos, bounds = qmm.sort_ids(ids, 3)
+    one = ids[:, 0].contiguous()
+    for name, y in (("combine", qmm.gather_sorted(x, pos, bounds)), ("combine_backward", qmm.combine(h, pos, w, base=x)),
+                    ("embed_backward", qmm.embed(x, qmm.F32, 12, 32, one)), ("lora_backward", qmm.lora(x, a, b, one))):
+        assert not y.requires_grad, name
+    for call, name in ((qmm.gather_sorted, "combine"), (qmm.combine, "combine_backward"), (qmm.embed, "embed_backward"),
+                       (qmm.lora, "lora_backward")):
+        assert name in call.__doc__ and "autograd" in call.__doc__
