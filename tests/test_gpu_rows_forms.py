@@ -102,3 +102,33 @@ def test_results_require_no_gradient_as_documented():
     for call, name in ((qmm.gather_sorted, "combine"), (qmm.combine, "combine_backward"), (qmm.embed, "embed_backward"),
                        (qmm.lora, "lora_backward")):
         assert name in call.__doc__ and "autograd" in call.__doc__
+
+
+# ------------------------------------------------------------------------------------------------
+# Gradient of the gather
+# ------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("n,top_k,n_exp,k", [(1, 1, 1, 1), (9, 8, 16, 33), (64, 2, 8, 256)])
+def test_gather_gradient(n, top_k, n_exp, k, dtype):
+    """combine without weights against the gradient's formula, rows past the valid pairs (which no token owns) NaN;
+    and against differences: the gather is linear, so those of any step have no error of their own."""
+    g = gen(n + k)
+    ids = some_ids(g, n * top_k, n_exp, bad=0.2).view(n, top_k)
+    _, pos, bounds = qmm.sort_ids(dev(ids), n_exp)
+    d = normal(g, n * top_k, k, dtype=dtype)
+    d[int(bounds[-1]):] = float("nan")
+    dx = qmm.combine(dev(d), pos)
+    want, mag = ref.combine(d, pos.cpu(), None, None)
+    ref.check(dx, want, top_k, mag, "dx")
+    x, step = normal(g, n, k, dtype=dtype), normal(g, n, k, dtype=dtype)
+    valid = int(bounds[-1])
+
+    def loss(v):
+        xs = qmm.gather_sorted(dev(v), pos, bounds).cpu().double()
+        return float((xs[:valid] * d[:valid].double()).sum())
+
+    slope = loss(x + step) - loss(x)
+    moved = (x + step).double() - x.double()   # as the type holds it
+    # dx off by the bound of ref.check: top_k + 2 roundings of fp32, then one of the type; 64-bit sums beside it
+    rel = (top_k + 2) * ref.U32 + (torch.finfo(dtype).eps if dtype != F32 else 0.0) + 1e-12
+    assert abs(slope - float((dx.cpu().double() * moved).sum())) <= rel * float((mag * moved.abs()).sum()) + 1e-9
