@@ -6,7 +6,7 @@ import torch
 import block_quantized_matmul_quantize_amd as qmm
 import rows_util as ref
 import synth
-from test_gpu_rows import BF16, F16, F32, dev, gen, normal, some_ids
+from test_gpu_rows import BF16, F16, F32, dev, gen, lora_case, lora_terms, normal, some_ids
 
 pytestmark = pytest.mark.gpu
 
@@ -132,3 +132,49 @@ def test_gather_gradient(n, top_k, n_exp, k, dtype):
     # dx off by the bound of ref.check: top_k + 2 roundings of fp32, then one of the type; 64-bit sums beside it
     rel = (top_k + 2) * ref.U32 + (torch.finfo(dtype).eps if dtype != F32 else 0.0) + 1e-12
     assert abs(slope - float((dx.cpu().double() * moved).sum())) <= rel * float((mag * moved.abs()).sum()) + 1e-9
+
+
+# ------------------------------------------------------------------------------------------------
+# One gradient of the adapters alone
+# ------------------------------------------------------------------------------------------------
+ELEM = {F32: qmm.F32, F16: qmm.F16, BF16: qmm.BF16}
+
+
+def backward_of(x, dy, h, a, b, ids, scale, shape, dx=None, da=None, db=None):
+    """qmm_lora_backward itself, which takes each gradient or leaves it out; the inputs that the wanted ones do
+    not need may be None.  The workspace has its stated size, and what is behind it stays."""
+    n, k, rows, rank, na, xt, wt = shape
+    size, guard = qmm.lora_backward_workspace(n, k, rows, rank, na), 4096
+    ws = torch.full((size + guard,), 77, dtype=torch.uint8, device="cuda")
+    p = [None if t is None else t.data_ptr() for t in (x, dy, h, a, b, ids, scale, dx, da, db)]
+    st = qmm.lib().qmm_lora_backward(ELEM[xt], ELEM[wt], p[0], p[1], p[2], n, k, p[3], p[4], rows, rank, na, p[5], p[6],
+                                     None, p[7], p[8], p[9], ws.data_ptr(), size, qmm._stream())
+    assert st == 0, qmm.lib().qmm_last_error()
+    assert bool((ws[size:] == 77).all())
+
+
+# several workgroups an adapter, as many or more for one gradient as for both; none; few rows an adapter; no rows
+@pytest.mark.parametrize("n,k,rows,rank,na", [(1300, 130, 72, 16, 1), (2100, 4104, 2000, 40, 1), (513, 256, 512, 12, 2),
+                                              (3000, 100, 520, 128, 3), (157, 300, 1000, 33, 57), (0, 64, 40, 8, 2)])
+@pytest.mark.parametrize("xt,wt", [(F32, F32), (F32, F16), (BF16, BF16), (F16, F16)])
+def test_lora_backward_of_one_gradient(n, k, rows, rank, na, xt, wt):
+    x, a, b, ids, scale, _, dy, _ = lora_case(n + k, n, k, rows, rank, na, xt, wt)
+    h = ref.lora(x, a, b, ids, scale, None)[2].float()
+    none = (ids < 0) | (ids >= na)
+    x[none], dy[none], h[none] = float("nan"), float("nan"), float("nan")
+    want, mag, most = ref.lora_backward(x, dy, h, a, b, ids, scale, None)
+    xd, dyd, hd, ad, bd, idd, sd = (dev(t) for t in (x, dy, h, a, b, ids, scale))
+    shape = (n, k, rows, rank, na, xt, wt)
+    da = torch.full(a.shape, 5.0, device="cuda")
+    backward_of(xd, dyd, None, None, bd, idd, sd, shape, da=da)
+    ref.check(da, want[1], lora_terms(rows, 3 * most), mag[1], "da alone")
+    db = torch.full(b.shape, 5.0, device="cuda")
+    backward_of(None, dyd, hd, None, None, idd, sd, shape, db=db)
+    ref.check(db, want[2], 9 * most + 8, mag[2], "db alone")
+    dx = torch.full(x.shape, 5.0, dtype=xt, device="cuda")
+    backward_of(None, dyd, None, ad, bd, idd, sd, shape, dx=dx)
+    ref.check(dx, want[0], lora_terms(rows, rank), mag[0], "dx alone")
+    again = torch.full(b.shape, 6.0, device="cuda"), torch.full(x.shape, 6.0, dtype=xt, device="cuda")
+    backward_of(None, dyd, hd, ad, bd, idd, sd, shape, dx=again[1], db=again[0])
+    assert torch.equal(again[1], dx)
+    ref.check(again[0], want[2], 9 * most + 8, mag[2], "db beside dx")
