@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import block_quantized_matmul_quantize_amd as qmm
+import rows_single
 import rows_util as ref
 import synth
 from test_gpu_rows import BF16, F16, F32, dev, gen, lora_case, lora_terms, normal, some_ids
@@ -178,3 +179,25 @@ def test_lora_backward_of_one_gradient(n, k, rows, rank, na, xt, wt):
     backward_of(None, dyd, hd, ad, bd, idd, sd, shape, dx=again[1], db=again[0])
     assert torch.equal(again[1], dx)
     ref.check(again[0], want[2], 9 * most + 8, mag[2], "db beside dx")
+
+
+# ------------------------------------------------------------------------------------------------
+# Precision of the adapters' products
+# ------------------------------------------------------------------------------------------------
+# ranks: every width of the first product's tiles and of the second's steps, filled and not
+@pytest.mark.parametrize("k,rows,rank", [(72, 264, 8), (2048, 130, 20), (333, 520, 32), (520, 100, 40), (264, 768, 64),
+                                         (4104, 72, 100), (200, 1000, 128)])
+@pytest.mark.parametrize("xt,wt", [(F32, F32), (F32, F16), (F32, BF16), (F16, F16), (BF16, BF16)])
+def test_lora_products_keep_every_bit_of_their_operands(k, rows, rank, xt, wt):
+    """Where every result is one chain of products, no sum hides what a product leaves out (SINGLE_TERMS)."""
+    na, n = 3, 120
+    x, a, b, ids, scale, dy = rows_single.inputs(k + rank, n, k, rows, rank, na, xt, wt)
+    wy, _, wh, _ = ref.lora(x, a, b, ids, scale, None)
+    y, h = qmm.lora(*(dev(t) for t in (x, a, b, ids, scale)), keep_h=True)
+    ref.check(h, wh, rows_single.SINGLE_TERMS, wh.abs(), "h")
+    ref.check(y, wy, rows_single.SINGLE_TERMS, wy.abs(), "y")
+    h = wh.float()
+    want, _, _ = ref.lora_backward(x, dy, h, a, b, ids, scale, None)
+    got = qmm.lora_backward(*(dev(t) for t in (x, dy, h, a, b, ids, scale)))
+    for u, v, name in zip(got, want, ("dx", "da", "db")):
+        ref.check(u, v, rows_single.SINGLE_TERMS, v.abs(), name)

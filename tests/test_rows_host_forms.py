@@ -5,6 +5,8 @@ import pytest
 import torch
 
 import block_quantized_matmul_quantize_amd as qmm
+import rows_single
+import rows_util as ref
 
 P = 0x100000       # aligned to every element
 Q = P + (1 << 20)
@@ -104,3 +106,23 @@ def test_embed_from_blocks_says_what_alignment_of_y_it_needs():
     assert "from blocks 16-byte aligned" in of_embed
     assert "from blocks 16 bytes" in text[text.index("Pointers need the alignment"):text.index("Row lengths")]
     assert "16-byte aligned" in qmm.embed.__doc__
+
+
+@pytest.mark.parametrize("k,rank", [(72, 8), (520, 40), (2048, 128)])
+def test_bound_of_single_products_refuses_two_parts_of_three(k, rank):
+    """The oracle's bound for one chain of products holds for fp32 products, and refuses one whose operands keep
+    16 of their 24 bits, at every size (among sums of k products such a loss would pass)."""
+    x, a, b, ids, scale, _ = rows_single.inputs(k, 120, k, 264, rank, 3, torch.float32, torch.float32)
+    want = ref.lora(x, a, b, ids, scale, None)[2]
+    got = torch.stack([a[int(c)] @ row for c, row in zip(ids, x)])
+    ref.check(got, want, rows_single.SINGLE_TERMS, want.abs())
+
+    def cut(t):
+        return (t.view(torch.int32) & ~0xff).view(torch.float32)
+
+    for xx, aa in ((cut(x), a), (x, cut(a)), (cut(x), cut(a))):
+        got = torch.stack([aa[int(c)].double() @ row.double() for c, row in zip(ids, xx)])
+        off = (got - want).abs() > (rows_single.SINGLE_TERMS + 2) * ref.U32 * want.abs()
+        assert off.double().mean() > 0.5
+        with pytest.raises(AssertionError):
+            ref.check(got.float(), want, rows_single.SINGLE_TERMS, want.abs())
