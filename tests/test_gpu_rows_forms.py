@@ -1,9 +1,14 @@
-"""Forms of the row operators' calls on the GPU: the combine straight on the expert products' results, streams."""
+"""Forms of the row operators' calls on the GPU: the combine straight on the expert products' results, streams,
+single gradients, the precision of single products, the example's gradients."""
+import os
+import sys
+
 import numpy as np
 import pytest
 import torch
 
 import block_quantized_matmul_quantize_amd as qmm
+import oracle
 import rows_single
 import rows_util as ref
 import synth
@@ -201,3 +206,51 @@ def test_lora_products_keep_every_bit_of_their_operands(k, rows, rank, xt, wt):
     got = qmm.lora_backward(*(dev(t) for t in (x, dy, h, a, b, ids, scale)))
     for u, v, name in zip(got, want, ("dx", "da", "db")):
         ref.check(u, v, rows_single.SINGLE_TERMS, v.abs(), name)
+
+
+# ------------------------------------------------------------------------------------------------
+# The example
+# ------------------------------------------------------------------------------------------------
+def test_example_moves_along_each_gradient():
+    """One step of the example moves each trained tensor along the gradient that 64-bit autograd has for the layer
+    without quantized activations.  These are off by at most 1/254 of a block's largest value, 0.9 % of its
+    spread where that is 4 times the spread; three products deep and within dz that is below 3 %, and as random
+    as dz itself in the sums over rows.  A gradient that lacks a term, a scale or a row's sign is off by its own
+    size: the bound, 10 %, is between."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    sys.path.insert(0, os.path.join(root, "examples"))
+    try:
+        import adapted_layer as ex
+    finally:
+        sys.path.pop(0)
+    layer, n, g = ex.Layer(), 96, gen(21)
+    tokens = torch.randint(0, ex.VOCAB, (n,), generator=g, dtype=torch.int32)
+    tokens[-2:] = -1
+    requests = (torch.arange(n) * ex.REQUESTS // n).to(torch.int32)
+    requests[:4] = -1
+    top, experts = torch.topk(torch.randn((n, ex.N_EXP), generator=g), ex.TOP_K, dim=1)
+    gates, target = torch.softmax(top, 1), normal(g, n, ex.K)
+    args = [dev(t) for t in (tokens, requests, experts.to(torch.int32).contiguous(), gates, target)]
+    for _ in range(3):   # b begins at zero, where a has no gradient
+        layer.step(*args, 0.1)
+    trained = [t.cpu().double().requires_grad_() for t in (layer.a, layer.b, layer.extra)]
+    layer.step(*args, 0.1)
+    moved = [t.detach() - v.cpu().double() for t, v in zip(trained, (layer.a, layer.b, layer.extra))]
+
+    def values(w, qtype, rows):
+        return torch.from_numpy(oracle.dequantize(qtype, w.cpu().numpy(), rows, ex.K)).double().view(rows, ex.K)
+
+    a, b, extra = trained
+    table, proj = values(layer.table, qmm.Q6_K, ex.VOCAB), values(layer.proj, qmm.Q4_K, ex.K)
+    w = torch.stack([values(e, qmm.Q4_K, ex.K) for e in layer.experts])
+    tok = tokens.clamp(min=0).long()
+    x = (table[tok] * layer.unit + extra[tok]) * (tokens >= 0)[:, None]
+    req = requests.clamp(min=0).long()
+    low = torch.matmul(b[req], torch.matmul(a[req], x[:, :, None]))[:, :, 0] * (layer.scale.cpu().double()[req])[:, None]
+    y = x @ proj.t() / layer.norm + low * (requests >= 0)[:, None]
+    z = y
+    for j in range(ex.TOP_K):
+        z = z + gates[:, j:j + 1].double() * torch.matmul(w[experts[:, j]], y[:, :, None])[:, :, 0] / layer.norm
+    want = torch.autograd.grad(((z - target.double()) ** 2).mean(), trained)
+    for name, u, v in zip(("a", "b", "extra"), moved, want):
+        assert v.norm() > 0 and float((u / u.norm() - v / v.norm()).norm()) <= 0.1, name
