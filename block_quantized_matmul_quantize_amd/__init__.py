@@ -845,8 +845,8 @@ def lora(x, a, b, ids, scale=None, base=None, out=None, keep_h=False, ws=None):
     """out[i] = base[i] + scale[c] * b[c] @ (a[c] @ x[i]) with c = ids[i]; base[i] alone for a c outside
     [0, n_adapters).  x [n, k] and base, out [n, rows] of one dtype; a [n_adapters, rank, k] and
     b [n_adapters, rows, rank] of x's dtype (beside fp32 x: any); ids int32 [n]; scale fp32
-    [n_adapters]; out may be base.  keep_h: returns (out, fp32 a[c] @ x[i] [n, rank]) for
-    lora_backward: autograd does not record the call."""
+    [n_adapters]; out may be base.  Rows of one adapter are fastest as neighbours.  keep_h: returns
+    (out, fp32 a[c] @ x[i] [n, rank]) for lora_backward: autograd does not record the call."""
     e, w, n, k, na, rank, rows, ps = _lora_shapes(x, a, b, ids, scale)
     pb = _arg(base, x.dtype, (n, rows), "base")
     po = _arg(out, x.dtype, (n, rows), "out")

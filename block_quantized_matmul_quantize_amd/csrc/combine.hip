@@ -1,11 +1,12 @@
 // Rows to expert order and back: the gather of each token's row to the places of its (token, slot)
 // pairs, the weighted sum of a token's expert results, and that sum's gradient.  All of them move
-// rows and do at most three operations an element, so HBM bounds them: every row is read once (a
-// token's row once for all its slots) and written once, 16 bytes a lane where rows allow it; no LDS, as
-// nothing is shared between lanes but the sum of a weight's gradient.  2048 tokens x 8 slots of 2048
-// fp32 values: gather 24 us, combine onto a base 25 us (6.7 TB/s with the rows partly in the 256 MB
-// cache, 33 us and 5.0 TB/s, a copy's rate, on rows from HBM); the gradient of 4096 x 2 of 4096 bf16
-// values 31 us.
+// rows and do at most three operations an element, so HBM bounds them, 16 bytes a lane where rows allow it.
+// Gather and combine read every row once (a token's row once for all its slots) and write it once; the
+// gradient has a workgroup a pair, so it reads a token's dy once for each slot (from cache after the first).
+// No LDS, as nothing is shared between lanes but the sum of a weight's gradient.  2048 tokens x 8 slots of
+// 2048 fp32 values: gather 24 us, combine onto a base 25 us (6.7 TB/s with the rows partly in the 256 MB
+// cache, 34 us and 5.0 TB/s, a copy's rate, on rows from HBM); the gradient of 4096 x 2 of 4096 bf16
+// values 31 us.  A decode step (16 x 8 of 2048) is latency, 4.2 us: a token's rows are loaded one after the other.
 #include "common.hpp"
 #include "launch.hpp"
 #include "rowtypes.hpp"

@@ -5,7 +5,9 @@
 // The lookup reads each named row's bytes and writes y, a few operations a value: launch latency bounds
 // a step's 8 tokens (3 us), HBM the large calls (2048 rows of 4096 Q6_K values into fp32: 11 us, 40 MB
 // at 3.7 TB/s, 83 % of it the output).  A thread decodes 8 neighbouring values, so that it stores 16
-// or 32 bytes and finds their scale once.
+// or 32 bytes and finds their scale once.  Tables of elements, 2048 rows of 4096 values into fp32: 12.5 us
+// from fp32 (5.4 TB/s), 10.4 us from bf16; one value a thread, where rows are no multiple of 8 values or an
+// address none of 16 bytes: 20.7 us (4092 and 4095 fp32 values).
 #include "common.hpp"
 #include "launch.hpp"
 #include "rowtypes.hpp"

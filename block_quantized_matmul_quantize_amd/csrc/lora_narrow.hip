@@ -5,11 +5,12 @@
 // adapter, which L2 holds), so HBM bounds the large calls and latency the small ones.  A workgroup
 // takes the rows of one adapter in a window of 64 and a slice of K; its four waves take turns at 32 K
 // values of all its rows, read straight into the operand registers of the matrix instructions (nothing
-// is read twice within a workgroup, so LDS would serve no reuse), several steps in flight.  The waves'
-// sums meet in LDS, in a fixed order.
+// is read twice within a workgroup, so LDS would serve no reuse), two or four steps in flight; one from rank
+// 33 on where a tile has more than 32 rows, and from rank 65 on.  The waves' sums meet in LDS, in a fixed order.
 //
 // 2048 rows of 4096 fp32 values at rank 16: 10.8 us (3.1 TB/s); 8192 rows of 4096 bf16 values at rank
-// 64, transposed: 24 us (2.8 TB/s); 32 rows of 64 adapters: 4.6 us.
+// 64, transposed: 20 us in runs of 256 rows (3.3 TB/s), 24 us in runs of any length; 32 rows of 64 adapters:
+// 4.6 us.  At rank 64 nothing is in flight while a step is multiplied, which keeps these from a copy's rate.
 #include "launch.hpp"
 #include "lora_parts.hpp"
 #include "sort_rows.hpp"

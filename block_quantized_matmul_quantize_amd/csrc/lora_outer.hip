@@ -9,9 +9,9 @@
 // their sums up in LDS in a fixed order.  An adapter with many rows and few columns is split over
 // several workgroups, whose sums a second launch adds up.
 //
-// 8192 rows of 4 adapters, x and dy of 4096 bf16 values (134 MB): 24 us at rank 16 (5.6 TB/s), 45 us at
+// 8192 rows of 4 adapters, x and dy of 4096 bf16 values (134 MB): 24 us at rank 16 (5.6 TB/s), 46 us at
 // rank 64, where the parts of h and dh, read once for each block of columns, are 200 MB from L2 beside
-// it (with 64 columns a block instead of 128: 70 us), 63 us for 4096 rows at rank 128.
+// it (with 64 columns a block instead of 128: 70 us), 70 us for 4096 rows at rank 128.
 #include "launch.hpp"
 #include "lora_parts.hpp"
 
@@ -186,16 +186,17 @@ __global__ __launch_bounds__(256) void join_kernel(const float *__restrict__ par
 }
 
 
-
 // Workgroups an adapter's rows are split over: 256 in all, while each wave keeps two steps of the
-// average adapter's rows.
+// average adapter's rows.  This rule and the next go by the average: the host does not know the segments.
+// Where one adapter of a large pool has all the rows, its few workgroups walk them alone (2048 rows at rank
+// 16, 4096 bf16 columns: 62 us in a pool of 64, 11 + 3 us in a pool of one).
 int splits_of(int64_t n, int64_t n_adapters, int64_t blocks) {
     int64_t s = 256 / (blocks * n_adapters), most = n / n_adapters / 256;
     if (s > most) s = most;
     return s < 1 ? 1 : s > 16 ? 16 : (int)s;
 }
 // With few rows an adapter the four waves of a workgroup take a block of columns each instead of steps of
-// rows that are not there (157 rows of 57 adapters at rank 64, 4625 columns: 36 us, 51 us with steps; from
+// rows that are not there (157 rows of 57 adapters at rank 64, 4625 columns: 36-41 us, 51 us with steps; from
 // 64 rows an adapter on, every wave has a step or two of its own).
 bool spread_of(int64_t n, int64_t n_adapters) { return n / n_adapters < 64; }
 int rank_tiles(int64_t rank) { return lora_padded_rank(rank) / 16; }

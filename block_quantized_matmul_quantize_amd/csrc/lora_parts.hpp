@@ -15,6 +15,11 @@ namespace qmm {
 // an adapter (key n_adapters) form a tile of their own, or none.  Found by one ballot per key bit from
 // 256 bytes of ids, so every wave does it for itself: no sort is launched before the forward pass, and
 // a step of single tokens (each row its own adapter) spreads over as many workgroups as it has tiles.
+//
+// So rows of one request should be neighbours.  In random order a window of many adapters has tiles of one or
+// two rows, each a product of 16 that reads its adapter again: 2048 rows of 64 adapters at rank 16,
+// 4096 -> 14336 columns, take 63 + 420 us forward, 11 + 46 us in runs of 256; backward 216 + 121 us for the two
+// products, 39 + 16 us in runs.  (The gradients of A and B take the rows sorted.)
 constexpr int kWindow = 64;
 
 struct Tiles {

@@ -10,9 +10,17 @@
 // or 128 bytes a row at a time, straight from the accumulators: column q of the lanes' pieces is one
 // matrix instruction's 16 columns.
 //
-// 2048 rows into 14336 fp32 columns at rank 16: 45 us (5.2 TB/s, a copy's rate); 8192 rows into 4096
-// bf16 columns at rank 64: 30 us, backward 33 (runs of 256 rows) to 44 us (runs of any length); 32 rows
-// of 64 adapters into 4096 columns: 5.9 us.
+// 2048 rows into 14336 fp32 columns at rank 16: 46 us (5.1 TB/s, a copy's rate); 8192 rows into 4096
+// bf16 columns at rank 64: 31 us, backward 33 (runs of 256 rows) to 45 us (runs of any length); 32 rows
+// of 64 adapters into 4096 columns: 5.2 us.
+//
+// Beyond rank 32 registers bound it too: the parts of all ranks and of a lane's four columns are held at
+// once, and with two waves a SIMD (256 registers) 53 of the 75 instances spill some.  Vector registers
+// spilled: up to 13 at ranks up to 32; at ranks 33-64 forward up to 34 and backward 44-64 (bf16 matrices
+// 4-16); at ranks 65-128 forward 67-85 and backward 124-144 with fp16 matrices, 0-25 and 57-77 with bf16 ones,
+// none with fp32 ones, which have one wave a SIMD.  4096 rows into 4096 columns, backward, by the types of the
+// rows and matrices: rank 64 bf16 20, fp16 34, fp32 / bf16 31, fp32 / fp16 50, fp32 46 us; rank 128 40, 65, 54,
+// 79, 67 us.  Forward: rank 64 21, 25, 29, 34, 35 us; rank 128 32, 55, 39, 66, 72 us.
 #include "launch.hpp"
 #include "lora_parts.hpp"
 

@@ -321,6 +321,8 @@ qmm_status qmm_embed_backward(int dy_type, const void *dy, int64_t n, int64_t k,
  *   db[c] = scale[c] * sum of dy[i] h[i]^T (fp32 [n_adapters][rows][rank]),
  *   over the rows i of adapter c; zeros for an adapter without rows.  dx, da and db may each be NULL
  *   (not computed).
+ * Rows of one adapter should be neighbours: among 64 consecutive rows each adapter's are one product,
+ *   which reads its matrices again.
  * Products are taken on exact bf16 parts of the operands, so that fp32 values keep their 24 bits.  An
  *   infinity or NaN makes the results of its own row (in the gradients: of its adapter) not finite, NaN
  *   where an infinity would do too, and those of no other.
